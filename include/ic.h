@@ -61,7 +61,9 @@ typedef int ic_status;
 #define IC_ERR_TIMEOUT (-5)     /* a device-side bounded wait gave up          */
 #define IC_ERR_BOUNDS (-6)      /* a debug-bounds build caught an index out of range */
 
-typedef enum { IC_F32 = 0, IC_BF16 = 1, IC_E4M3 = 2 } ic_dtype;
+/* IC_MXF4: 4-bit microscaled latent cache rows (see ic_cache_append), a format of the
+ * paged calls only. */
+typedef enum { IC_F32 = 0, IC_BF16 = 1, IC_E4M3 = 2, IC_MXF4 = 3 } ic_dtype;
 
 /* Message of the last failed call on this host thread ("" if none). */
 const char* ic_last_error(void);
@@ -104,6 +106,9 @@ ic_status ic_device_status(void* stream);
 #define IC_K_ATTN_MLA_KV8 13
 #define IC_K_PACK_KV 14
 #define IC_K_FILL_VALID 15
+#define IC_K_RMS_NORM 16
+#define IC_K_CACHE_APPEND 17
+#define IC_K_ATTN_MLA_KV4 18
 ic_status ic_trace_begin(void* stream, int capacity);
 long ic_trace_end(float* ms, int* kinds, double* work, int capacity);
 
@@ -389,8 +394,136 @@ ic_status ic_decode_step(const char* pattern, const ic_stack_desc* desc, const i
                          int nlayers, int* t_cache, void* workspace, size_t ws_bytes,
                          void* stream);
 
-/* Recommended workspace bytes for ic_layer_stack / ic_decode_step. */
+/* Recommended workspace bytes for ic_layer_stack / ic_decode_step / ic_decode_step_paged. */
 size_t ic_stack_workspace_size(const ic_stack_desc* desc);
+
+/*
+ * RMS norm of a layer's input, with the residual's addition before it and an e4m3
+ * output beside (or instead of) the plain one:
+ *   h = x + residual (h = x without one)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ * in fp32; the norm is of the unrounded sum.  Row r of a matrix starts at r * its ld.
+ *   x        [rows, n] dt (IC_BF16 or IC_F32)
+ *   residual [rows, n] dt or NULL
+ *   weight   [n] w_dt (IC_BF16 or IC_F32)
+ *   h        [rows, n] dt or NULL: the sum, rounded to dt (may be x or residual itself)
+ *   y        [rows, n] dt or NULL (may be x itself)
+ *   codes    [rows, n] uint8 or NULL: y as e4m3 codes, quantised from fp32 as
+ *            ic_quant_e4m3_rows quantises a row, per group of 128 values
+ *   scales   [rows, ceil(n / 128)] f32, dense (with codes): the groups' scales
+ * At least one of y, codes and h is wanted.  Outputs may be inputs where the list says
+ * so, with the same ld; otherwise they must not overlap.  n >= 1; every ld >= n (that
+ * of an absent matrix is ignored); eps >= 0; |h| < 1.8e19 / sqrt(n), so that the sum of
+ * squares stays finite.  Any alignment of the type is taken; rows of a multiple of 8
+ * values, up to 16384, at 16-byte aligned addresses (codes: 8) are read only once.
+ */
+ic_status ic_rms_norm(const void* x, long ld_x, const void* residual, long ld_r, ic_dtype dt,
+                      const void* weight, ic_dtype w_dt, float eps, long rows, int n, void* h,
+                      long ld_h, void* y, long ld_y, uint8_t* codes, long ld_codes,
+                      float* scales, void* stream);
+
+/*
+ * Appends tokens to the caches: the latent rows and / or the indexer keys of `rows`
+ * tokens go to rows slots[i] of the caches, with the position rotation applied on the
+ * way.  A cache is a matrix of num_slots rows: the pool of a paged cache (slot = page
+ * number * page size + place in the page) or a contiguous one.
+ *   slots [rows] int64: token i is written to row slots[i]; a token whose slot is
+ *         negative or >= num_slots is not written (a padded batch uses -1).  Slots
+ *         of one call are distinct: of two tokens with one slot, every 16 bytes hold
+ *         either's.  Other rows are left as they were.
+ *   pos   [rows] int32 positions, rope [rope_rows, 64] f32: row p holds cos(p f_i), i =
+ *         0..31, then sin(p f_i).  A token with a position outside [0, rope_rows) is not
+ *         written.  rope == NULL: no rotation, pos is ignored.
+ *   kv    [rows, ld_kv >= 576] bf16, or NULL for no latent rows: 512 latent dims, then
+ *         64 dims that are rotated: dims (2i, 2i + 1) of them by angle i, or (i, i + 32)
+ *         with IC_ROPE_KV_HALVES.  (a, b) -> (a cos - b sin, b cos + a sin), in fp32.
+ *   kv_cache, ld_cache, kv_dt: the latent rows' cache:
+ *         IC_BF16  576 values; ld_cache in elements, >= 576, a multiple of 8
+ *         IC_E4M3  the 656-byte row of ic_pack_kv_e4m3; ld_cache in bytes, of 16
+ *         IC_MXF4  400 bytes (OCP microscaling, MXFP4); ld_cache in bytes, of 16:
+ *           bytes   0..255  the 512 latent dims as e2m1 codes, dim 2i in the low half of
+ *                           byte i, rounded to nearest, ties to even
+ *           bytes 256..271  16 e8m0 scales, one per 32 dims: the smallest power of two
+ *                           that puts the largest magnitude at 6 or less (at least
+ *                           2^-127; 255, and codes 0, if a value is not finite)
+ *           bytes 272..399  the 64 rotated dims, bf16
+ *   k     [rows, ld_k >= 128] bf16, or NULL for no keys: indexer keys, of which dims
+ *         0..63 are rotated as above (IC_ROPE_K_HALVES selects (i, i + 32))
+ *   k_cache [num_slots, 128], k_dt: IC_BF16, or IC_E4M3 codes with one scale per key in
+ *         k_scale [num_slots], quantised as by ic_quant_e4m3_rows but from the rotated
+ *         fp32 values
+ * kv, kv_cache and k_cache are 16-byte aligned, k is 8-byte aligned; ld_kv is a multiple
+ * of 8 and ld_k of 4.
+ */
+#define IC_ROPE_KV_HALVES 1
+#define IC_ROPE_K_HALVES 2
+ic_status ic_cache_append(long rows, const long* slots, const int* pos, const float* rope,
+                          long rope_rows, const void* kv, long ld_kv, void* kv_cache,
+                          long ld_cache, ic_dtype kv_dt, const void* k, long ld_k, void* k_cache,
+                          float* k_scale, ic_dtype k_dt, long num_slots, int flags,
+                          void* stream);
+
+/*
+ * Paged caches.  Token s of sequence b is row page * page_size + s % page_size of the
+ * pool, with page = block_table[b * ld_table + s / page_size].  Everything that
+ * pointers name is read on the device, so a captured call may be replayed with other
+ * lengths and pages.
+ *   block_table [batch, ld_table >= max_pages] int32, device
+ *   seq_lens    [batch] int32, device: tokens of each sequence; 0 (or less) is an empty one,
+ *               lengths above the limits of a call are clamped to them
+ *   page_size   a power of two from 16 to 1024;  num_pages  pages of the pool
+ * Pages past a sequence's length are not looked up.  An entry outside [0, num_pages)
+ * within it is an error of the caller that reads nothing out of bounds: its keys score
+ * 0, its latent rows are skipped.
+ */
+typedef struct {
+  const int* block_table;
+  long ld_table;
+  int max_pages;
+  const int* seq_lens;
+  int page_size;
+  int num_pages;
+} ic_paging;
+
+/*
+ * ic_indexer_scores for one query per sequence, at its last token, over paged keys:
+ *   scores[b, s] = sum_h w[b, h] * max(0, q[b, h, :] . k[row of (b, s), :]),
+ *   s < min(seq_lens[b], max_len); other columns are left as they were (ic_topk_varlen
+ *   with valid_len = seq_lens selects from the written ones).
+ *   q [batch, H, D], q_scale [batch, H], w [batch, H], k [num_pages * page_size, D],
+ *   k_scale [num_pages * page_size]: as ic_indexer_scores; dt = IC_BF16 or IC_E4M3
+ *   (H = 64, D = 128; IC_F32 -> IC_ERR_UNSUPPORTED)
+ *   scores [batch, ld] f32, ld >= max_len;  1 <= max_len <= max_pages * page_size
+ */
+ic_status ic_indexer_scores_paged(const void* q, const float* q_scale, const void* k,
+                                  const float* k_scale, const float* w, ic_dtype dt, int batch,
+                                  int H, int D, const ic_paging* paging, int max_len,
+                                  float* scores, long ld, void* stream);
+
+/*
+ * The absorbed-MLA form of ic_sparse_attn over a paged latent cache: index entries are
+ * token numbers of the query's own sequence; entries outside [0, seq_lens[b]) are
+ * skipped.  A query without entries gets zeros and lse = -inf, whatever the cache holds.
+ *   q [batch, rows, 16, 576] bf16; kv: the pool, dt = IC_BF16 (ld_kv in elements),
+ *   IC_E4M3 or IC_MXF4 (ld_kv in bytes), rows as ic_cache_append writes them;
+ *   idx [batch, rows, k] int32, k <= 2048; out, lse, workspace as ic_sparse_attn.
+ */
+ic_status ic_sparse_attn_paged(const void* q, const void* kv, long ld_kv,
+                               const ic_paging* paging, const int* idx, ic_dtype dt, int batch,
+                               int rows, int heads, int dk, int dv, int k, float scale, void* out,
+                               float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * ic_decode_step over paged caches, for sequences of different lengths: layer l's k_idx
+ * (and k_scale) and kv are pools of paging->num_pages pages, its one query per sequence
+ * sits at the sequence's last token (already appended).  desc->L bounds the lengths (at
+ * most max_pages * page_size); desc->idx_dtype is IC_BF16 or IC_E4M3, desc->attn_dtype
+ * IC_BF16, IC_E4M3 or IC_MXF4; IC_STACK_FUSED_TOPK is not supported.  Other arguments,
+ * the routing, the workspace and the errors are as ic_decode_step.
+ */
+ic_status ic_decode_step_paged(const char* pattern, const ic_stack_desc* desc,
+                               const ic_paging* paging, const ic_layer_io* layers, int nlayers,
+                               int* t_cache, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

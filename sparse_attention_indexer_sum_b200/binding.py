@@ -26,7 +26,7 @@ IC_ERR_WORKSPACE = -3
 IC_ERR_CUDA = -4
 IC_ERR_TIMEOUT = -5
 IC_ERR_BOUNDS = -6
-IC_F32, IC_BF16, IC_E4M3 = 0, 1, 2
+IC_F32, IC_BF16, IC_E4M3, IC_MXF4 = 0, 1, 2, 3
 
 # names declared in include/ic.h (checked against the header by the tests)
 EXPORTS = ("ic_last_error", "ic_version", "ic_device_status", "ic_trace_begin", "ic_trace_end",
@@ -35,7 +35,9 @@ EXPORTS = ("ic_last_error", "ic_version", "ic_device_status", "ic_trace_begin", 
            "ic_topk_varlen", "ic_sparse_attn",
            "ic_attn_workspace_size",
            "ic_layer_stack", "ic_decode_step", "ic_stack_workspace_size",
-           "ic_sparse_attn_noalloc", "ic_layer_stack_rows", "ic_layer_stack_varlen")
+           "ic_sparse_attn_noalloc", "ic_layer_stack_rows", "ic_layer_stack_varlen",
+           "ic_rms_norm", "ic_cache_append", "ic_indexer_scores_paged", "ic_sparse_attn_paged",
+           "ic_decode_step_paged")
 
 
 class ICError(RuntimeError):
@@ -59,7 +61,14 @@ class ic_stack_desc(ctypes.Structure):
                 ("scale", ctypes.c_float), ("flags", ctypes.c_int)]
 
 
+class ic_paging(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_long),
+                ("max_pages", ctypes.c_int), ("seq_lens", ctypes.c_void_p),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int)]
+
+
 IC_STACK_FUSED_TOPK = 1
+IC_ROPE_KV_HALVES, IC_ROPE_K_HALVES = 1, 2
 
 
 _lib = None
@@ -105,6 +114,16 @@ def lib() -> ctypes.CDLL:
     L.ic_stack_workspace_size.argtypes = [ctypes.POINTER(ic_stack_desc)]
     L.ic_stack_workspace_size.restype = S
     L.ic_sparse_attn_noalloc.argtypes = [P, P, Lg, P, P, I, I, I, I, I, I, I, I, F, P, P, P]
+    L.ic_rms_norm.argtypes = [P, Lg, P, Lg, I, P, I, F, Lg, I, P, Lg, P, Lg, P, Lg, P, P]
+    L.ic_cache_append.argtypes = [Lg, P, P, P, Lg, P, Lg, P, Lg, I, P, Lg, P, P, I, Lg, I, P]
+    PG = ctypes.POINTER(ic_paging)
+    L.ic_indexer_scores_paged.argtypes = [P, P, P, P, P, I, I, I, I, PG, I, P, Lg, P]
+    L.ic_sparse_attn_paged.argtypes = [P, P, Lg, PG, P, I, I, I, I, I, I, I, F, P, P, P, S, P]
+    L.ic_decode_step_paged.argtypes = [ctypes.c_char_p, ctypes.POINTER(ic_stack_desc), PG,
+                                       ctypes.POINTER(ic_layer_io), I, P, P, S, P]
+    for name in ("ic_rms_norm", "ic_cache_append", "ic_indexer_scores_paged",
+                 "ic_sparse_attn_paged", "ic_decode_step_paged"):
+        getattr(L, name).restype = I
     for name in ("ic_device_status", "ic_quant_e4m3_rows", "ic_pack_kv_e4m3", "ic_indexer_scores",
                  "ic_topk",
                  "ic_topk_varlen", "ic_indexer_topk",
@@ -167,7 +186,8 @@ def ic_device_status(stream=None):
 KIND_NAMES = {1: "indexer_tc_bf16", 2: "indexer_tc_e4m3", 3: "indexer_f32", 4: "fill_masked",
               5: "topk", 6: "attn_mla", 7: "attn_combine", 8: "attn_f32", 9: "quant_e4m3",
               10: "topk_merge", 11: "indexer_topk_bf16", 12: "indexer_topk_e4m3",
-              13: "attn_mla_kv8", 14: "pack_kv_e4m3", 15: "fill_valid"}
+              13: "attn_mla_kv8", 14: "pack_kv_e4m3", 15: "fill_valid", 16: "rms_norm",
+              17: "cache_append", 18: "attn_mla_kv4"}
 
 
 def ic_trace_begin(capacity: int = 4096, stream=None):
@@ -435,3 +455,279 @@ def decode_step_graph(pattern: str, desc: ic_stack_desc, layers: list[dict], t_c
     with torch.cuda.graph(graph, capture_error_mode="relaxed"):
         ic_decode_step(pattern, desc, layers, t_cache, workspace)
     return graph
+
+
+# ------------------------------------------------------------------ around the path
+KV4_ROW_BYTES = 400
+_DT = {torch.float32: IC_F32, torch.bfloat16: IC_BF16}
+_KV_ROW = {IC_BF16: 2 * 576, IC_E4M3: KV8_ROW_BYTES, IC_MXF4: KV4_ROW_BYTES}
+
+
+def _one_device(*ts):
+    """The CUDA device that every given tensor lives on (a ValueError otherwise)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device (got one on %s)" % t.device)
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors are on %s and %s" % (dev, t.device))
+    return dev
+
+
+class _On:
+    """Runs the body with `dev` current and allocations made for `stream`; yields the raw stream."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.held = dev, stream, []
+
+    def __enter__(self):
+        if self.dev.index != torch.cuda.current_device():
+            self.held.append(torch.cuda.device(self.dev))
+            self.held[-1].__enter__()
+        if self.stream is not None:
+            s = self.stream
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(int(s), device=self.dev)
+            elif s.device != self.dev:
+                self.__exit__(None, None, None)
+                raise ValueError("stream of %s, tensors on %s" % (s.device, self.dev))
+            self.held.append(torch.cuda.stream(s))
+            self.held[-1].__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        while self.held:
+            self.held.pop().__exit__(*exc)
+
+
+def _rows2d(t, name, n, dtypes):
+    """(rows, row stride) of t [..., n] whose leading dims are dense over the row stride."""
+    if t.dtype not in dtypes or t.dim() < 1 or t.shape[-1] != n:
+        raise ValueError("%s must be %s [..., %d]" % (name, " or ".join(map(str, dtypes)), n))
+    if n > 1 and t.stride(-1) != 1:
+        raise ValueError("%s rows must be contiguous" % name)
+    rows, ld = 1, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size != 1:
+            if ld is None:
+                ld = stride
+            elif stride != ld * rows:
+                raise ValueError("%s rows must be evenly spaced" % name)
+            rows *= size
+    return rows, n if ld is None else ld
+
+
+def _pool(t, name, dtypes, row_bytes=0):
+    """(slots, row stride in elements, row length) of a cache [slots, w] or [pages, page, w]."""
+    if t.dim() not in (2, 3) or t.dtype not in dtypes:
+        raise ValueError("%s must be %s [slots, width] or [pages, page_size, width]" % (
+            name, " or ".join(map(str, dtypes))))
+    w = t.shape[-1]
+    if w * t.element_size() < row_bytes:
+        raise ValueError("%s rows must hold %d bytes" % (name, row_bytes))
+    rows, ld = _rows2d(t, name, w, dtypes)
+    return rows, ld, w
+
+
+def ic_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, h=None, y=None, codes=None,
+                scales=None, stream=None):
+    """RMS norm of x [..., n] (+ residual): h = x + residual, y = h / sqrt(mean h^2 + eps) *
+    weight.  Writes the outputs that are given (h, y like x; codes uint8 [..., n] with
+    scales f32 [..., ceil(n / 128)]), or a new y if none is; returns (y, codes, scales)."""
+    n = x.shape[-1]
+    rows, ld_x = _rows2d(x, "x", n, (torch.bfloat16, torch.float32))
+    if weight.dtype not in _DT or tuple(weight.shape) != (n,) or not weight.is_contiguous():
+        raise ValueError("weight must be bf16 or fp32 [%d], contiguous" % n)
+    dev = _one_device(x, weight, residual, h, y, codes, scales)
+    with _On(dev, stream) as st:
+        if h is None and y is None and codes is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        lds = []
+        for t, name, dt in ((residual, "residual", x.dtype), (h, "h", x.dtype), (y, "y", x.dtype),
+                            (codes, "codes", torch.uint8)):
+            if t is not None and t.shape != x.shape:
+                raise ValueError("%s must have x's shape" % name)
+            lds.append(0 if t is None else _rows2d(t, name, n, (dt,))[1])
+        if (codes is None) != (scales is None):
+            raise ValueError("codes and scales go together")
+        if scales is not None and (scales.dtype != torch.float32 or not scales.is_contiguous() or
+                                   tuple(scales.shape) != tuple(x.shape[:-1]) + (-(-n // 128),)):
+            raise ValueError("scales must be fp32 %s, contiguous" %
+                             (tuple(x.shape[:-1]) + (-(-n // 128),),))
+        _check(lib().ic_rms_norm(_p(x), ld_x, _p(residual), lds[0], _DT[x.dtype], _p(weight),
+                                 _DT[weight.dtype], float(eps), rows, n, _p(h), lds[1], _p(y),
+                                 lds[2], _p(codes), lds[3], _p(scales), st))
+    return y, codes, scales
+
+
+def rope_table(positions: int, theta: float = 10000.0, device=None) -> torch.Tensor:
+    """cos | sin [positions, 64] f32 of position * theta^(-i / 32), i = 0..31, for
+    ic_cache_append; the angles are taken in 64 bits, so far positions keep theirs."""
+    inv = float(theta) ** (-torch.arange(32, dtype=torch.float64, device=device) / 32)
+    ang = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([ang.cos(), ang.sin()], dim=1).float()
+
+
+def ic_cache_append(slots, *, kv=None, kv_cache=None, kv_dtype=None, k=None, k_cache=None,
+                    k_scale=None, pos=None, rope=None, kv_halves: bool = False,
+                    k_halves: bool = False, stream=None):
+    """Writes the latent rows kv [rows, 576] and / or the indexer keys k [rows, 128] (bf16)
+    of `rows` tokens to rows slots [rows] (int64; negative: not written) of kv_cache
+    ([slots, w] or [pages, page_size, w]; kv_dtype IC_BF16, IC_E4M3 or IC_MXF4) and k_cache
+    (bf16, or uint8 e4m3 codes with k_scale), rotated by rope [P, 64] at positions pos."""
+    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("slots must be int64 [rows], contiguous")
+    rows = slots.shape[0]
+    dev = _one_device(slots, kv, kv_cache, k, k_cache, k_scale, pos, rope)
+    if (kv is None) != (kv_cache is None) or (k is None) != (k_cache is None):
+        raise ValueError("kv goes with kv_cache, k with k_cache")
+    if kv is None and k is None:
+        raise ValueError("nothing to append")
+    if (rope is None) != (pos is None):
+        raise ValueError("rope goes with pos")
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or rope.shape[1] != 64 or \
+                not rope.is_contiguous():
+            raise ValueError("rope must be fp32 [positions, 64], contiguous")
+        if pos.dtype != torch.int32 or tuple(pos.shape) != (rows,) or not pos.is_contiguous():
+            raise ValueError("pos must be int32 [rows], contiguous")
+    sizes, ld_kv, ld_cache, ld_k, k_dt = set(), 0, 0, 0, IC_BF16
+    if kv is not None:
+        if kv_dtype is None:
+            kv_dtype = IC_BF16 if kv_cache.dtype == torch.bfloat16 else None
+        if kv_dtype not in (IC_BF16, IC_E4M3, IC_MXF4):
+            raise ValueError("kv_dtype must be IC_BF16, IC_E4M3 or IC_MXF4")
+        n, ld_kv = _rows2d(kv, "kv", 576, (torch.bfloat16,))
+        slot_count, ld_cache, _ = _pool(kv_cache, "kv_cache", (
+            torch.bfloat16 if kv_dtype == IC_BF16 else torch.uint8,), _KV_ROW[kv_dtype])
+        if n != rows:
+            raise ValueError("kv must have %d rows" % rows)
+        sizes.add(slot_count)
+    if k is not None:
+        n, ld_k = _rows2d(k, "k", 128, (torch.bfloat16,))
+        slot_count, ld, w = _pool(k_cache, "k_cache", (torch.bfloat16, torch.uint8))
+        if n != rows or w != 128 or ld != 128:
+            raise ValueError("k must have %d rows, k_cache dense rows of 128" % rows)
+        sizes.add(slot_count)
+        if k_cache.dtype == torch.uint8:
+            k_dt = IC_E4M3
+            if k_scale is None or k_scale.dtype != torch.float32 or \
+                    k_scale.numel() != slot_count or not k_scale.is_contiguous():
+                raise ValueError("an e4m3 key cache needs k_scale, fp32, one per slot")
+    if len(sizes) != 1:
+        raise ValueError("kv_cache and k_cache differ in their number of slots")
+    if rows == 0:
+        return
+    with _On(dev, stream) as st:
+        _check(lib().ic_cache_append(
+            rows, _p(slots), _p(pos), _p(rope), 0 if rope is None else rope.shape[0], _p(kv),
+            ld_kv, _p(kv_cache), ld_cache, IC_BF16 if kv_dtype is None else kv_dtype, _p(k), ld_k,
+            _p(k_cache), _p(k_scale) if k_dt == IC_E4M3 else None, k_dt, sizes.pop(),
+            (IC_ROPE_KV_HALVES if kv_halves else 0) | (IC_ROPE_K_HALVES if k_halves else 0), st))
+
+
+def make_paging(block_table, seq_lens, page_size: int, num_pages: int) -> ic_paging:
+    """ic_paging over block_table [batch, max_pages] int32 and seq_lens [batch] int32 (device
+    tensors that the caller keeps alive)."""
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [batch, max_pages] with contiguous rows")
+    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (block_table.shape[0],) or \
+            not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be int32 [batch], contiguous")
+    ld = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
+    return ic_paging(block_table=block_table.data_ptr(), ld_table=ld,
+                     max_pages=block_table.shape[1], seq_lens=seq_lens.data_ptr(),
+                     page_size=int(page_size), num_pages=int(num_pages))
+
+
+def _pages(rows, page_size, name):
+    if page_size < 1 or rows % page_size:
+        raise ValueError("%s must hold whole pages of %d rows" % (name, page_size))
+    return rows // page_size
+
+
+def ic_indexer_scores_paged(q, k_cache, w, block_table, seq_lens, *, page_size: int, scores=None,
+                            q_scale=None, k_scale=None, stream=None):
+    """Indexer scores [B, L] of one query per sequence (at its last token) over paged keys:
+    q [B, 64, 128] or [B, 1, 64, 128], w [B(, 1), 64], k_cache [slots, 128] or [pages, page_size,
+    128] (bf16, or uint8 e4m3 codes with q_scale [B(, 1), 64] and k_scale, one per slot).
+    Writes columns s < seq_lens[b] of `scores` (new: [B, max_pages * page_size]) only."""
+    _contig(q, w, q_scale, k_scale)
+    slots, ld, d = _pool(k_cache, "k_cache", (torch.bfloat16, torch.uint8))
+    B = block_table.shape[0]
+    H = q.shape[-2]
+    if q.dtype != k_cache.dtype or d != q.shape[-1] or ld != d:
+        raise ValueError("q and k_cache must have one type and dense rows of one length")
+    if q.numel() != B * H * d or w.dtype != torch.float32 or w.numel() != B * H:
+        raise ValueError("q must be [B, H, D] and w fp32 [B, H] with B = %d sequences" % B)
+    fp8 = q.dtype == torch.uint8
+    if fp8 and (q_scale is None or k_scale is None or q_scale.dtype != torch.float32 or
+                k_scale.dtype != torch.float32 or q_scale.numel() != B * H or
+                k_scale.numel() != slots):
+        raise ValueError("e4m3 keys need fp32 q_scale [B, H] and k_scale [slots]")
+    dev = _one_device(q, k_cache, w, block_table, seq_lens, scores, q_scale, k_scale)
+    pg = make_paging(block_table, seq_lens, page_size, _pages(slots, page_size, "k_cache"))
+    with _On(dev, stream) as st:
+        most = block_table.shape[1] * page_size
+        if scores is None:
+            scores = torch.empty((B, most), dtype=torch.float32, device=dev)
+        if scores.dtype != torch.float32 or scores.dim() != 2 or scores.shape[0] != B or \
+                (scores.shape[1] > 1 and scores.stride(1) != 1):
+            raise ValueError("scores must be fp32 [%d, L] with contiguous rows" % B)
+        ld = scores.stride(0) if B > 1 else scores.shape[1]
+        _check(lib().ic_indexer_scores_paged(
+            _p(q), _p(q_scale) if fp8 else None, _p(k_cache), _p(k_scale) if fp8 else None, _p(w),
+            IC_E4M3 if fp8 else IC_BF16, B, H, d, ctypes.byref(pg), min(scores.shape[1], most),
+            _p(scores), ld, st))
+    return scores
+
+
+def ic_sparse_attn_paged(q, kv_cache, idx, block_table, seq_lens, scale: float, *, page_size: int,
+                         kv_dtype=None, out=None, lse=None, workspace=None, stream=None):
+    """Absorbed-MLA sparse attention over a paged latent cache: q [B, R, 16, 576] bf16, idx
+    [B, R, k] int32 token numbers of each query's own sequence (entries outside it are
+    skipped), kv_cache [slots, w] or [pages, page_size, w] of kv_dtype (IC_BF16; uint8 rows:
+    IC_E4M3 or IC_MXF4).  workspace: ic_attn_workspace_size bytes let few queries be split."""
+    _contig(q, idx, out, lse)
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or idx.dtype != torch.int32 or \
+            idx.dim() != 3 or idx.shape[:2] != q.shape[:2] or q.shape[0] != block_table.shape[0]:
+        raise ValueError("q must be bf16 [B, R, H, D] and idx int32 [B, R, k], B = %d sequences" %
+                         block_table.shape[0])
+    if kv_dtype is None:
+        kv_dtype = IC_BF16 if kv_cache.dtype == torch.bfloat16 else None
+    if kv_dtype not in (IC_BF16, IC_E4M3, IC_MXF4):
+        raise ValueError("kv_dtype must be IC_BF16, IC_E4M3 or IC_MXF4")
+    slots, ld, _ = _pool(kv_cache, "kv_cache",
+                         (torch.bfloat16 if kv_dtype == IC_BF16 else torch.uint8,),
+                         _KV_ROW[kv_dtype])
+    B, R, H, dk = q.shape
+    dev = _one_device(q, kv_cache, idx, block_table, seq_lens, out, lse, workspace)
+    pg = make_paging(block_table, seq_lens, page_size, _pages(slots, page_size, "kv_cache"))
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((B, R, H, 512), dtype=torch.bfloat16, device=dev)
+        if out.dtype != torch.bfloat16 or tuple(out.shape) != (B, R, H, 512):
+            raise ValueError("out must be bf16 %s" % ((B, R, H, 512),))
+        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, R, H)):
+            raise ValueError("lse must be fp32 %s" % ((B, R, H),))
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib().ic_sparse_attn_paged(
+            _p(q), _p(kv_cache), ld, ctypes.byref(pg), _p(idx), kv_dtype, B, R, H, dk, 512,
+            idx.shape[-1], float(scale), _p(out), _p(lse), _p(workspace), ws_bytes, st))
+    return out
+
+
+def ic_decode_step_paged(pattern: str, desc: ic_stack_desc, paging: ic_paging, layers: list[dict],
+                         t_cache, workspace, stream=None):
+    """Decode step over paged caches (make_paging; desc.decode = 1, desc.L bounds the lengths):
+    layers hold the pools as k_idx, k_scale and kv."""
+    arr = _layers(layers)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().ic_decode_step_paged(pattern.encode(), ctypes.byref(desc), ctypes.byref(paging),
+                                      arr, len(layers), _p(t_cache), _p(workspace), ws_bytes,
+                                      _stream(stream)))

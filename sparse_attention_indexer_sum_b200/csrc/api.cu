@@ -149,7 +149,7 @@ static ic_status run_attn(const void* q, const void* kv, long ld_kv, const void*
                           size_t ws_bytes, long long valid_entries, cudaStream_t stream) {
   if (!v)
     return launch_attn_mla(q, kv, ld_kv, idx, batch, rows, Lkv, k, scale, out, lse, ws, ws_bytes,
-                           valid_entries, stream, dt == IC_E4M3);
+                           valid_entries, stream, dt == IC_E4M3 ? kFmtE4m3 : kFmtBf16);
   return launch_attn_f32(static_cast<const float*>(q), static_cast<const float*>(kv), ld_kv,
                          static_cast<const float*>(v), idx, batch, rows, heads, dk, dv, Lkv, k,
                          scale, static_cast<float*>(out), lse, stream);
@@ -166,6 +166,85 @@ static ic_status check_desc(const ic_stack_desc* d, bool decode) {
                                            : "layer stack needs desc->decode = 0 (use ic_decode_step)");
   if (!decode && d->batch != 1) return fail(IC_ERR_UNSUPPORTED, "stack: prefill batch must be 1");
   return IC_OK;
+}
+
+// ------------------------------------------------------------------ paged calls
+static ic_status check_paging(const ic_paging* p, const char* who) {
+  if (!p || !p->block_table || !p->seq_lens)
+    return fail(IC_ERR_INVALID_ARG, "%s: NULL paging, block table or lengths", who);
+  if (p->page_size < 16 || p->page_size > 1024 || (p->page_size & (p->page_size - 1)) != 0)
+    return fail(IC_ERR_INVALID_ARG, "%s: page_size must be a power of two in [16, 1024] (got %d)",
+                who, p->page_size);
+  if (p->num_pages < 1 || p->max_pages < 1 || p->ld_table < p->max_pages)
+    return fail(IC_ERR_INVALID_ARG, "%s: bad paging (num_pages %d max_pages %d ld_table %ld)", who,
+                p->num_pages, p->max_pages, p->ld_table);
+  if (static_cast<long>(p->num_pages) * p->page_size > 0x7fffffffL ||
+      static_cast<long>(p->max_pages) * p->page_size > 0x7fffffffL)
+    return fail(IC_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 rows", who);
+  return IC_OK;
+}
+
+static PagedArgs paged_args(const ic_paging* p, long max_len) {
+  PagedArgs a;
+  a.table = p->block_table;
+  a.ld_table = p->ld_table;
+  a.seq_lens = p->seq_lens;
+  a.shift = __builtin_ctz(static_cast<unsigned>(p->page_size));
+  a.num_pages = p->num_pages;
+  const long most = static_cast<long>(p->max_pages) * p->page_size;
+  a.max_len = static_cast<int>(max_len < most ? max_len : most);
+  return a;
+}
+
+static ic_status check_indexer_paged(const void* q, const float* q_scale, const void* k,
+                                     const float* k_scale, const float* w, ic_dtype dt, int batch,
+                                     int H, int D, const ic_paging* pg, int max_len) {
+  if (!q || !k || !w) return fail(IC_ERR_INVALID_ARG, "indexer_paged: NULL tensor");
+  if (dt != IC_BF16 && dt != IC_E4M3)
+    return fail(IC_ERR_UNSUPPORTED, "indexer_paged: needs bf16 or e4m3 keys (got %d)",
+                static_cast<int>(dt));
+  if (H != 64 || D != 128)
+    return fail(IC_ERR_UNSUPPORTED, "indexer_paged: needs H=64, D=128 (got %d, %d)", H, D);
+  if (dt == IC_E4M3 && (!q_scale || !k_scale))
+    return fail(IC_ERR_INVALID_ARG, "indexer_paged: e4m3 inputs need q_scale and k_scale");
+  if (!aligned(q, 16) || !aligned(k, 16))
+    return fail(IC_ERR_INVALID_ARG, "indexer_paged: q and k must be 16-byte aligned");
+  if (batch < 1 || max_len < 1 ||
+      max_len > static_cast<long>(pg->max_pages) * pg->page_size)
+    return fail(IC_ERR_INVALID_ARG, "indexer_paged: bad sizes (batch %d max_len %d)", batch,
+                max_len);
+  if (static_cast<long>(batch) * 64 > 0x7fffffffL)
+    return fail(IC_ERR_UNSUPPORTED, "indexer_paged: too many sequences");
+  return IC_OK;
+}
+
+static ic_status check_attn_paged(const void* q, const void* kv, long ld_kv, const int* idx,
+                                  ic_dtype dt, int batch, int rows, int heads, int dk, int dv,
+                                  int k, const void* out) {
+  if (!q || !kv || !idx || !out) return fail(IC_ERR_INVALID_ARG, "attn_paged: NULL tensor");
+  if (batch < 1 || rows < 0 || k < 1) return fail(IC_ERR_INVALID_ARG, "attn_paged: bad sizes");
+  if ((dt != IC_BF16 && dt != IC_E4M3 && dt != IC_MXF4) || heads != 16 || dk != 576 || dv != 512)
+    return fail(IC_ERR_UNSUPPORTED,
+                "attn_paged: needs a bf16, e4m3 or mxf4 cache, 16 heads, dk 576, dv 512 "
+                "(got %d, %d, %d, %d)", static_cast<int>(dt), heads, dk, dv);
+  const long least = dt == IC_BF16 ? 576 : dt == IC_E4M3 ? KV8_ROW_BYTES : KV4_ROW_BYTES;
+  if (!aligned(q, 16) || !aligned(kv, 16) || ld_kv < least || ld_kv % (dt == IC_BF16 ? 8 : 16))
+    return fail(IC_ERR_INVALID_ARG,
+                "attn_paged: q and cache rows must be 16-byte aligned, ld_kv at least %ld", least);
+  if (!aligned(out, 4)) return fail(IC_ERR_INVALID_ARG, "attn_paged: out must be 4-byte aligned");
+  if (k > 2048) return fail(IC_ERR_UNSUPPORTED, "attn_paged: needs k <= 2048");
+  if (static_cast<long>(batch) * rows > 0x7fffffffL)
+    return fail(IC_ERR_UNSUPPORTED, "attn_paged: too many queries");
+  return IC_OK;
+}
+
+static ic_status run_attn_paged(const void* q, const void* kv, long ld_kv, const PagedArgs& pg,
+                                const int* idx, ic_dtype dt, int batch, int rows, int k,
+                                float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                                cudaStream_t stream) {
+  const int fmt = dt == IC_MXF4 ? kFmtMxf4 : dt == IC_E4M3 ? kFmtE4m3 : kFmtBf16;
+  return launch_attn_mla(q, kv, ld_kv, idx, batch, rows, 0, k, scale, out, lse, ws, ws_bytes, -1,
+                         stream, fmt, nullptr, 0, &pg);
 }
 
 // Rows per score block for a workspace of ws_bytes: scores [rows, L] fp32.
@@ -275,6 +354,66 @@ static ic_status run_stack(const char* pattern, const ic_stack_desc* d, const ic
   return IC_OK;
 }
 
+// The decode step over paged caches: an F layer scores its sequences in blocks of as
+// many score rows as the workspace holds, each selected by its own length.
+static ic_status run_decode_paged(const char* pattern, const ic_stack_desc* d,
+                                  const ic_paging* paging, const ic_layer_io* layers, int nlayers,
+                                  int* t_cache, void* workspace, size_t ws_bytes,
+                                  cudaStream_t stream) {
+  ic_status st = check_desc(d, true);
+  if (st) return st;
+  st = check_paging(paging, "decode_step_paged");
+  if (st) return st;
+  if (d->flags & IC_STACK_FUSED_TOPK)
+    return fail(IC_ERR_UNSUPPORTED, "decode_step_paged: IC_STACK_FUSED_TOPK is not supported");
+  std::vector<char> kinds;
+  st = parse_pattern(pattern, &kinds);
+  if (st) return st;
+  if (static_cast<int>(kinds.size()) != nlayers)
+    return fail(IC_ERR_INVALID_ARG, "pattern has %zu layers, nlayers is %d", kinds.size(), nlayers);
+  if (!layers || !t_cache) return fail(IC_ERR_INVALID_ARG, "stack: NULL layers or t_cache");
+  for (int l = 0; l < nlayers; ++l) {
+    const ic_layer_io& io = layers[l];
+    if (kinds[l] == 'F') {
+      st = check_indexer_paged(io.q_idx, io.q_scale, io.k_idx, io.k_scale, io.w, d->idx_dtype,
+                               d->batch, d->H, d->D, paging, d->L);
+      if (st) return fail(st, "layer %d: %s", l, ic_last_error());
+    }
+    if (io.v) return fail(IC_ERR_UNSUPPORTED, "layer %d: paged caches are absorbed MLA (v = NULL)", l);
+    st = check_attn_paged(io.q, io.kv, d->ld_kv, t_cache, d->attn_dtype, d->batch, 1, d->heads,
+                          d->dk, d->dv, d->k, io.out);
+    if (st) return fail(st, "layer %d: %s", l, ic_last_error());
+  }
+  const long rb = score_rows(ws_bytes, d->L, d->batch);
+  if (!workspace || rb < 1)
+    return fail(IC_ERR_WORKSPACE, "stack: workspace of %zu bytes holds no score row of %d floats",
+                ws_bytes, d->L);
+  float* scores = static_cast<float*>(workspace);
+  const PagedArgs pg = paged_args(paging, d->L);
+  const size_t qrow_b = static_cast<size_t>(d->H) * d->D * elem_bytes(d->idx_dtype);
+  for (int l = 0; l < nlayers; ++l) {
+    const ic_layer_io& io = layers[l];
+    for (long u0 = 0; kinds[l] == 'F' && u0 < d->batch; u0 += rb) {
+      const int nu = static_cast<int>(d->batch - u0 < rb ? d->batch - u0 : rb);
+      PagedArgs part = pg;
+      part.table += u0 * pg.ld_table;
+      part.seq_lens += u0;
+      st = launch_indexer_tc_paged(d->idx_dtype == IC_E4M3,
+                                   static_cast<const uint8_t*>(io.q_idx) + u0 * qrow_b,
+                                   io.q_scale ? io.q_scale + u0 * d->H : nullptr, io.k_idx,
+                                   io.k_scale, io.w + u0 * d->H, nu, part, scores, d->L, stream);
+      if (st) return st;
+      st = launch_topk(scores, nu, d->L, d->L, -1, d->k, t_cache + u0 * d->k, stream,
+                       part.seq_lens);
+      if (st) return st;
+    }
+    st = run_attn_paged(io.q, io.kv, d->ld_kv, pg, t_cache, d->attn_dtype, d->batch, 1, d->k,
+                        d->scale, io.out, io.lse, workspace, ws_bytes, stream);
+    if (st) return st;
+  }
+  return IC_OK;
+}
+
 // Packed sequences (cu: host [nseq + 1]) of a stack in shared launches.
 // F layers walk the packed query rows in blocks that fit the score workspace and
 // touch at most IC_MAXSEG sequences: one indexer launch over the block's segments
@@ -309,7 +448,7 @@ static ic_status run_stack_varlen_shared(const std::vector<char>& kinds, const i
                 ws_bytes, ld);
   float* scores = static_cast<float*>(workspace);
   int* valid = reinterpret_cast<int*>(scores + rb * ld);
-  const bool kv8 = d->attn_dtype == IC_E4M3;
+  const int fmt = d->attn_dtype == IC_E4M3 ? kFmtE4m3 : kFmtBf16;
   const bool f32_idx = d->idx_dtype == IC_F32, f32_attn = d->attn_dtype == IC_F32;
   const size_t qe = f32_attn ? 4 : 2;  // q and out: fp32 (MQA) or bf16 (MLA)
   const size_t arow_b = static_cast<size_t>(d->heads) * d->dk * qe;
@@ -391,7 +530,7 @@ static ic_status run_stack_varlen_shared(const std::vector<char>& kinds, const i
                                      static_cast<int>(asegs.size()))
                    : launch_attn_mla(qg, io.kv, d->ld_kv, t_cache + r0 * d->k, 1,
                                      static_cast<int>(nr), d->L, d->k, d->scale, og, lg, workspace,
-                                     ws_bytes, valid_entries, stream, kv8, asegs.data(),
+                                     ws_bytes, valid_entries, stream, fmt, asegs.data(),
                                      static_cast<int>(asegs.size()));
       if (st) return st;
     }
@@ -425,6 +564,8 @@ ic_status ic_device_status(void* stream) {
                   v == kErrBoundsGather ? "index-list entry outside the cache"
                   : v == kErrBoundsTma  ? "TMA tile coordinate outside the tensor"
                   : v == kErrBoundsTopk ? "top-k output slot outside the row"
+                  : v == kErrBoundsPage ? "page number outside the pool"
+                  : v == kErrBoundsSlot ? "cache slot or position outside its cache or table"
                                         : "merge slot or piece count out of range");
     return fail(IC_ERR_TIMEOUT, "device error word %d (a bounded device wait gave up)", v);
   }
@@ -612,6 +753,142 @@ ic_status ic_decode_step(const char* pattern, const ic_stack_desc* desc, const i
                          int nlayers, int* t_cache, void* workspace, size_t ws_bytes,
                          void* stream) {
   return run_stack(pattern, desc, layers, nlayers, t_cache, workspace, ws_bytes, stream, true);
+}
+
+ic_status ic_rms_norm(const void* x, long ld_x, const void* residual, long ld_r, ic_dtype dt,
+                      const void* weight, ic_dtype w_dt, float eps, long rows, int n, void* h,
+                      long ld_h, void* y, long ld_y, uint8_t* codes, long ld_codes,
+                      float* scales, void* stream) {
+  if (!x || !weight || (!h && !y && !codes))
+    return fail(IC_ERR_INVALID_ARG, "rms_norm: NULL tensor (x, weight, or no output at all)");
+  if ((codes != nullptr) != (scales != nullptr))
+    return fail(IC_ERR_INVALID_ARG, "rms_norm: codes and scales go together");
+  if ((dt != IC_BF16 && dt != IC_F32) || (w_dt != IC_BF16 && w_dt != IC_F32))
+    return fail(IC_ERR_UNSUPPORTED, "rms_norm: x and weight must be bf16 or fp32");
+  if (rows < 0 || n < 1 || ld_x < n || (residual && ld_r < n) || (h && ld_h < n) ||
+      (y && ld_y < n) || (codes && ld_codes < n) || !(eps >= 0.f))
+    return fail(IC_ERR_INVALID_ARG, "rms_norm: bad sizes (rows %ld n %d, every ld >= n, eps >= 0)",
+                rows, n);
+  if (rows > 0x7fffffffL) return fail(IC_ERR_UNSUPPORTED, "rms_norm: too many rows");
+  const size_t e = dt == IC_F32 ? 4 : 2;
+  if (!aligned(x, e) || !aligned(residual, e) || !aligned(h, e) || !aligned(y, e) ||
+      !aligned(weight, w_dt == IC_F32 ? 4 : 2) || !aligned(scales, 4))
+    return fail(IC_ERR_INVALID_ARG, "rms_norm: tensors must be aligned to their type");
+  if ((h && ((h == x && ld_h != ld_x) || (h == residual && ld_h != ld_r))) ||
+      (y && (y == h || y == residual || (y == x && (ld_y != ld_x || h == x)))))
+    return fail(IC_ERR_INVALID_ARG, "rms_norm: outputs overlap each other or an input");
+  RmsNormArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.h = h;
+  a.y = y;
+  a.codes = codes;
+  a.scales = scales;
+  a.ld_x = ld_x;
+  a.ld_r = residual ? ld_r : 0;
+  a.ld_h = h ? ld_h : 0;
+  a.ld_y = y ? ld_y : 0;
+  a.ld_c = codes ? ld_codes : 0;
+  a.rows = rows;
+  a.n = n;
+  a.f32 = dt == IC_F32;
+  a.w_f32 = w_dt == IC_F32;
+  a.eps = eps;
+  return launch_rms_norm(a, static_cast<cudaStream_t>(stream));
+}
+
+ic_status ic_cache_append(long rows, const long* slots, const int* pos, const float* rope,
+                          long rope_rows, const void* kv, long ld_kv, void* kv_cache,
+                          long ld_cache, ic_dtype kv_dt, const void* k, long ld_k, void* k_cache,
+                          float* k_scale, ic_dtype k_dt, long num_slots, int flags,
+                          void* stream) {
+  if (!slots || (!kv && !k) || (kv && !kv_cache) || (k && !k_cache) || (rope && !pos))
+    return fail(IC_ERR_INVALID_ARG, "cache_append: NULL tensor");
+  if (rows < 0 || num_slots < 1 || (rope && rope_rows < 1))
+    return fail(IC_ERR_INVALID_ARG, "cache_append: bad sizes (rows %ld num_slots %ld rope_rows %ld)",
+                rows, num_slots, rope_rows);
+  if (rows > 0x7fffffffL) return fail(IC_ERR_UNSUPPORTED, "cache_append: too many rows");
+  if (flags & ~(IC_ROPE_KV_HALVES | IC_ROPE_K_HALVES))
+    return fail(IC_ERR_INVALID_ARG, "cache_append: unknown flags %d", flags);
+  if (!aligned(slots, 8) || !aligned(pos, 4) || !aligned(rope, 4))
+    return fail(IC_ERR_INVALID_ARG, "cache_append: slots, pos and rope must be aligned to their type");
+  if (kv) {
+    if (kv_dt != IC_BF16 && kv_dt != IC_E4M3 && kv_dt != IC_MXF4)
+      return fail(IC_ERR_UNSUPPORTED, "cache_append: latent cache must be bf16, e4m3 or mxf4");
+    const long least = kv_dt == IC_BF16 ? 576 : kv_dt == IC_E4M3 ? KV8_ROW_BYTES : KV4_ROW_BYTES;
+    if (ld_kv < 576 || ld_kv % 8 || ld_cache < least || ld_cache % (kv_dt == IC_BF16 ? 8 : 16) ||
+        !aligned(kv, 16) || !aligned(kv_cache, 16))
+      return fail(IC_ERR_INVALID_ARG,
+                  "cache_append: latent rows must be 16-byte aligned, ld_kv >= 576, ld_cache >= %ld",
+                  least);
+  }
+  if (k) {
+    if (k_dt != IC_BF16 && k_dt != IC_E4M3)
+      return fail(IC_ERR_UNSUPPORTED, "cache_append: key cache must be bf16 or e4m3");
+    if (k_dt == IC_E4M3 && !k_scale)
+      return fail(IC_ERR_INVALID_ARG, "cache_append: an e4m3 key cache needs k_scale");
+    if (ld_k < 128 || ld_k % 4 || !aligned(k, 8) || !aligned(k_cache, 16) || !aligned(k_scale, 4))
+      return fail(IC_ERR_INVALID_ARG, "cache_append: keys must be 8-byte aligned rows, ld_k >= 128");
+  }
+  AppendArgs a;
+  a.slots = slots;
+  a.pos = pos;
+  a.rope = rope;
+  a.kv = static_cast<const __nv_bfloat16*>(kv);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.kv_cache = static_cast<uint8_t*>(kv_cache);
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.k_scale = k_scale;
+  a.rows = rows;
+  a.rope_rows = rope_rows;
+  a.num_slots = num_slots;
+  a.ld_kv = ld_kv;
+  a.ld_k = ld_k;
+  a.ld_cache = kv_dt == IC_BF16 ? 2 * ld_cache : ld_cache;
+  a.kv_fmt = !kv                ? kFmtBf16
+             : kv_dt == IC_MXF4 ? kFmtMxf4
+             : kv_dt == IC_E4M3 ? kFmtE4m3
+                                : kFmtBf16;
+  a.k_fp8 = k_dt == IC_E4M3;
+  a.kv_halves = (flags & IC_ROPE_KV_HALVES) != 0;
+  a.k_halves = (flags & IC_ROPE_K_HALVES) != 0;
+  return launch_cache_append(a, static_cast<cudaStream_t>(stream));
+}
+
+ic_status ic_indexer_scores_paged(const void* q, const float* q_scale, const void* k,
+                                  const float* k_scale, const float* w, ic_dtype dt, int batch,
+                                  int H, int D, const ic_paging* paging, int max_len,
+                                  float* scores, long ld, void* stream) {
+  ic_status st = check_paging(paging, "indexer_paged");
+  if (st) return st;
+  st = check_indexer_paged(q, q_scale, k, k_scale, w, dt, batch, H, D, paging, max_len);
+  if (st) return st;
+  if (!scores || ld < max_len)
+    return fail(IC_ERR_INVALID_ARG, "indexer_paged: scores is NULL or ld (%ld) below max_len (%d)",
+                ld, max_len);
+  return launch_indexer_tc_paged(dt == IC_E4M3, q, q_scale, k, k_scale, w, batch,
+                                 paged_args(paging, max_len), scores, ld,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+ic_status ic_sparse_attn_paged(const void* q, const void* kv, long ld_kv,
+                               const ic_paging* paging, const int* idx, ic_dtype dt, int batch,
+                               int rows, int heads, int dk, int dv, int k, float scale, void* out,
+                               float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  ic_status st = check_paging(paging, "attn_paged");
+  if (st) return st;
+  st = check_attn_paged(q, kv, ld_kv, idx, dt, batch, rows, heads, dk, dv, k, out);
+  if (st) return st;
+  return run_attn_paged(q, kv, ld_kv, paged_args(paging, 0x7fffffffL), idx, dt, batch, rows, k,
+                        scale, out, lse, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+ic_status ic_decode_step_paged(const char* pattern, const ic_stack_desc* desc,
+                               const ic_paging* paging, const ic_layer_io* layers, int nlayers,
+                               int* t_cache, void* workspace, size_t ws_bytes, void* stream) {
+  return run_decode_paged(pattern, desc, paging, layers, nlayers, t_cache, workspace, ws_bytes,
+                          static_cast<cudaStream_t>(stream));
 }
 
 size_t ic_stack_workspace_size(const ic_stack_desc* d) {

@@ -107,16 +107,26 @@ struct AttnSegs {
 struct AttnNoSegs {
   int unused;
 };
-template <bool SEGS>
-using AttnSegParam = typename std::conditional<SEGS, AttnSegs, AttnNoSegs>::type;
+// How a query's index entries become cache rows: one batch of equal contexts, packed
+// sequences, or pages of a pool (PagedArgs, ic_internal.h).
+constexpr int kAddrDense = 0, kAddrSegs = 1, kAddrPaged = 2;
+template <int ADDR>
+using AttnAddrParam =
+    typename std::conditional<ADDR == kAddrPaged, PagedArgs,
+                              typename std::conditional<ADDR == kAddrSegs, AttnSegs,
+                                                        AttnNoSegs>::type>::type;
 
 // Latent rows of query row qrow: the first row's offset (in rows) and how many.
-template <bool SEGS>
-__device__ __forceinline__ void attn_kv_range(const AttnArgs& a, const AttnSegParam<SEGS>& sg,
+// Paged: row0 is the sequence's number, len its tokens.
+template <int ADDR>
+__device__ __forceinline__ void attn_kv_range(const AttnArgs& a, const AttnAddrParam<ADDR>& sg,
                                               long qrow, long& row0, int& len) {
-  if constexpr (!SEGS) {
+  if constexpr (ADDR == kAddrDense) {
     row0 = (qrow / a.R) * static_cast<long>(a.Lkv);
     len = a.Lkv;
+  } else if constexpr (ADDR == kAddrPaged) {
+    row0 = qrow / a.R;
+    len = min(sg.seq_lens[row0], sg.max_len);
   } else {
     int lo = 0, hi = sg.nseg - 1;
     while (lo < hi) {
@@ -129,6 +139,19 @@ __device__ __forceinline__ void attn_kv_range(const AttnArgs& a, const AttnSegPa
     row0 = sg.seg[lo].k0;
     len = sg.seg[lo].len;
   }
+}
+
+// Paged instances: zeros the rows of one tile stage of producer warp pw that receive
+// no copy, so that a NaN or infinity left there by an earlier query's row cannot
+// reach this one through 0 * NaN.  Only tiles with missing rows have any.
+__device__ __forceinline__ void attn_zero_rows(uint8_t* stage_rows, unsigned valid, int pw) {
+  unsigned miss = ~valid & (0xFFu << (8 * pw));
+  if (!miss) return;
+  for (; miss; miss &= miss - 1) {
+    uint4* row = reinterpret_cast<uint4*>(stage_rows + (__ffs(miss) - 1) * AT_ROWB);
+    for (int i = threadIdx.x & 31; i < AT_DK * 2 / 16; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();  // before a later copy lands where these stores went
 }
 
 // Dequantises the fp8 rows of one tile stage that belong to producer warp pw (rows
@@ -171,6 +194,64 @@ __device__ __forceinline__ void attn_dequant_rows(uint8_t* stage_rows, unsigned 
     *reinterpret_cast<uint4*>(row + 32 * lane + 16) = make_uint4(o[4], o[5], o[6], o[7]);
     if (lane < 8) *reinterpret_cast<uint4*>(row + 1024 + 16 * lane) = rope[r];
   }
+  __syncwarp();
+}
+
+// Paged: the pool row of token s (0 <= s < len) of sequence b, or -1 if its page
+// number lies outside the pool.
+__device__ __forceinline__ long attn_page_row(const PagedArgs& pg, long b, int s) {
+  const int page = __ldg(pg.table + b * pg.ld_table + (s >> pg.shift));
+  if (!in_bounds(page >= 0 && page < pg.num_pages, kErrBoundsPage) || page < 0 ||
+      page >= pg.num_pages)
+    return -1;
+  return (static_cast<long>(page) << pg.shift) + (s & ((1 << pg.shift) - 1));
+}
+
+// The same for the 4-bit rows (400 bytes at slot offset 768: 512 e2m1 codes, two a
+// byte with the even dim low, 16 e8m0 block scales, 64 bf16 rope dims).  Lane l owns
+// latent dims 16l..16l+15, half of block l / 2.  A code times a power of two is exact
+// in bf16.  Rows without a copy become zeros.
+__device__ __forceinline__ void attn_dequant_rows4(uint8_t* stage_rows, unsigned valid, int pw) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* rows = stage_rows + 8 * pw * AT_ROWB;
+  const unsigned mine = (valid >> (8 * pw)) & 0xFFu;
+  uint2 codes[8];
+  uint4 rope[8];
+  unsigned sc[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const uint8_t* raw = rows + r * AT_ROWB + (AT_ROWB - KV4_ROW_BYTES);
+    codes[r] = *reinterpret_cast<const uint2*>(raw + 8 * lane);
+    sc[r] = raw[256 + (lane >> 1)];
+    rope[r] = lane < 8 ? *reinterpret_cast<const uint4*>(raw + 272 + 16 * lane)
+                       : make_uint4(0, 0, 0, 0);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    uint8_t* row = rows + r * AT_ROWB;
+    uint32_t o[8];
+    if ((mine >> r) & 1u) {
+      const float s = e8m0_value(sc[r]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = i < 4 ? codes[r].x : codes[r].y;
+        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(
+            static_cast<__nv_fp4x2_storage_t>((w >> (8 * (i & 3))) & 0xFFu), __NV_E2M1);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
+        o[i] = *reinterpret_cast<uint32_t*>(&v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = 0u;
+      rope[r] = make_uint4(0, 0, 0, 0);
+    }
+    *reinterpret_cast<uint4*>(row + 32 * lane) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(row + 32 * lane + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+    if (lane < 8) *reinterpret_cast<uint4*>(row + 1024 + 16 * lane) = rope[r];
+  }
+  fence_proxy_async_smem();  // before the next copies land where these stores went
   __syncwarp();
 }
 
@@ -274,11 +355,13 @@ __device__ __forceinline__ void attn_load_indices(AttnSmem& sm, const AttnArgs& 
 // every tile -- one warp's bulk copies issue one lane at a time, so spreading a
 // tile over four warps quadruples the gather issue rate.  Producer 0 also owns
 // the per-item work: the next index list, the queries, the stage flags.
-// KV8: fp8 latent rows; SEGS: packed sequences (separate instances, so that the
-// bf16 form of one batch compiles without either)
-template <bool KV8, bool SEGS>
+// FMT: the latent rows' format; ADDR: packed sequences or pages (separate instances,
+// so that the bf16 form of one batch compiles without any of them)
+template <int FMT, int ADDR>
 __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
-                                              const AttnSegParam<SEGS>& sg) {
+                                              const AttnAddrParam<ADDR>& sg) {
+  constexpr bool RAW = FMT != kFmtBf16;  // rows that the producers expand to bf16
+  constexpr int RAW_BYTES = FMT == kFmtMxf4 ? KV4_ROW_BYTES : KV8_ROW_BYTES;
   const int lane = threadIdx.x & 31;
   const int pw = (threadIdx.x - AT_CONSUMERS) >> 5;
   volatile int* abort = &sm.abort;
@@ -304,7 +387,12 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.rawf[pend_stage]), pend_ph, abort,
                                            kErrTimeoutProducer)))
       return false;
-    attn_dequant_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
+    if constexpr (FMT == kFmtMxf4)
+      attn_dequant_rows4(&sm.kv[pend_stage][0][0], pend_valid, pw);
+    else
+      attn_dequant_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
+    if constexpr (FMT == kFmtE4m3 && ADDR == kAddrPaged)
+      attn_zero_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.full[pend_stage]));
     pend_stage = -1;
@@ -319,9 +407,10 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
     const int cnt = x.end - x.beg;
     long kr0;
     int lkv;
-    attn_kv_range<SEGS>(a, sg, x.qrow, kr0, lkv);
-    const __nv_bfloat16* kvb = a.kv + kr0 * a.ld_kv;
-    const uint8_t* kvb8 = reinterpret_cast<const uint8_t*>(a.kv) + kr0 * a.ld_kv;
+    attn_kv_range<ADDR>(a, sg, x.qrow, kr0, lkv);
+    const long kbase = ADDR == kAddrPaged ? 0 : kr0 * a.ld_kv;
+    const __nv_bfloat16* kvb = a.kv + kbase;
+    const uint8_t* kvb8 = reinterpret_cast<const uint8_t*>(a.kv) + kbase;
     // every producer is done with the previous item (and its index list)
     if (lane == 0) mbar_arrive(smem_u32(&sm.pitem));
     if (!mbar_wait(smem_u32(&sm.pitem), static_cast<uint32_t>(nitem & 1), abort, kErrTimeoutProducer))
@@ -361,29 +450,49 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
     }
     const int nt = ntiles > 0 ? ntiles : 1;  // an empty item still ends with one (empty) tile
     bool ok = true;
+    // paged: the pool row of this lane's entry of tile t (the page table is read one
+    // tile ahead, so that its latency hides behind the wait for a free stage)
+    auto pool_row = [&](int t) -> long {
+      const int j = t * AT_BK + lane;
+      const int s = (t < ntiles && j < cnt) ? ilist[j] : -1;
+      if (!in_bounds(s >= -1 && s < lkv, kErrBoundsGather) || s < 0 || s >= lkv) return -1;
+      if constexpr (ADDR == kAddrPaged) return attn_page_row(sg, kr0, s);
+      return s;
+    };
+    long prow = -1;
+    if constexpr (ADDR == kAddrPaged) prow = pool_row(0);
     for (int t = 0; t < nt; ++t) {
+      long pnext = -1;
+      if constexpr (ADDR == kAddrPaged) pnext = pool_row(t + 1);
       if (!mbar_wait(smem_u32(&sm.empty[stage]), ph ^ 1, abort, kErrTimeoutProducer)) {
         ok = false;
         break;
       }
-      const int j = t * AT_BK + lane;
-      int s = (t < ntiles && j < cnt) ? ilist[j] : -1;
-      if (!in_bounds(s >= -1 && s < lkv, kErrBoundsGather) || s >= lkv) s = -1;
+      long s;
+      if constexpr (ADDR == kAddrPaged) {
+        s = prow;
+        prow = pnext;
+      } else {
+        const int j = t * AT_BK + lane;
+        int e = (t < ntiles && j < cnt) ? ilist[j] : -1;
+        if (!in_bounds(e >= -1 && e < lkv, kErrBoundsGather) || e >= lkv) e = -1;
+        s = e;
+      }
       const unsigned valid = __ballot_sync(0xffffffffu, s >= 0);
       if (pw == 0 && lane == 0) {
         sm.vmask[stage] = valid;
         sm.last[stage] = (t == nt - 1);
       }
-      if constexpr (KV8) {
-        // the raw fp8 row lands in the slot's last 656 bytes; the warp dequantises
+      if constexpr (RAW) {
+        // the raw row lands in the slot's last RAW_BYTES bytes; the warp dequantises
         // its rows of the previous tile while these copies are in flight
         const uint32_t rb = smem_u32(&sm.rawf[stage]);
         if (lane == 0)
-          mbar_arrive_expect_tx(rb, __popc(valid & (0xFFu << (8 * pw))) * KV8_ROW_BYTES);
+          mbar_arrive_expect_tx(rb, __popc(valid & (0xFFu << (8 * pw))) * RAW_BYTES);
         __syncwarp();
         if (mine && s >= 0)
-          bulk_g2s(kv0 + (stage * AT_BK + lane) * AT_ROWB + (AT_ROWB - KV8_ROW_BYTES),
-                   kvb8 + static_cast<long>(s) * a.ld_kv, KV8_ROW_BYTES, rb);
+          bulk_g2s(kv0 + (stage * AT_BK + lane) * AT_ROWB + (AT_ROWB - RAW_BYTES),
+                   kvb8 + s * a.ld_kv, RAW_BYTES, rb);
         if (!dequant_pending()) {
           ok = false;
           break;
@@ -393,12 +502,15 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
         pend_valid = valid;
       } else {
         const uint32_t fb = smem_u32(&sm.full[stage]);
+        if constexpr (ADDR == kAddrPaged) {
+          attn_zero_rows(&sm.kv[stage][0][0], valid, pw);
+          __syncwarp();
+        }
         if (lane == 0)
           mbar_arrive_expect_tx(fb, __popc(valid & (0xFFu << (8 * pw))) * AT_ROW_BYTES);
         __syncwarp();
         if (mine && s >= 0)
-          bulk_g2s(kv0 + (stage * AT_BK + lane) * AT_ROWB, kvb + static_cast<long>(s) * a.ld_kv,
-                   AT_ROW_BYTES, fb);
+          bulk_g2s(kv0 + (stage * AT_BK + lane) * AT_ROWB, kvb + s * a.ld_kv, AT_ROW_BYTES, fb);
       }
       ++issued;
       if (++stage == AT_STAGES) {
@@ -408,13 +520,13 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
     }
     if (!ok) break;
   }
-  if (KV8 && !*abort) (void)dequant_pending();  // the last tile
+  if (RAW && !*abort) (void)dequant_pending();  // the last tile
   if (*abort) {
     // let every copy still in flight land before the CTA exits
     volatile int never = 0;
     const long n = issued < AT_STAGES ? issued : AT_STAGES;
     for (long j = issued - n; j < issued; ++j)
-      (void)mbar_wait(smem_u32(KV8 ? &sm.rawf[j % AT_STAGES] : &sm.full[j % AT_STAGES]),
+      (void)mbar_wait(smem_u32(RAW ? &sm.rawf[j % AT_STAGES] : &sm.full[j % AT_STAGES]),
                       static_cast<uint32_t>((j / AT_STAGES) & 1), &never, kErrTimeoutDrain);
     if (qloads > 0) (void)mbar_wait(smem_u32(&sm.qfull), (qloads - 1) & 1, &never, kErrTimeoutDrain);
     for (int b2 = 0; b2 < 2; ++b2)
@@ -637,9 +749,9 @@ __device__ __forceinline__ void attn_consumer(AttnSmem& sm, const AttnArgs& a) {
   }
 }
 
-template <bool KV8, bool SEGS>
+template <int FMT, int ADDR>
 __global__ void __launch_bounds__(AT_THREADS, 1)
-    attn_mla_kernel(const AttnArgs a, const __grid_constant__ AttnSegParam<SEGS> sg) {
+    attn_mla_kernel(const AttnArgs a, const __grid_constant__ AttnAddrParam<ADDR> sg) {
   extern __shared__ uint8_t at_smem_raw[];
   AttnSmem& sm = *reinterpret_cast<AttnSmem*>(
       (reinterpret_cast<uintptr_t>(at_smem_raw) + 127) & ~static_cast<uintptr_t>(127));
@@ -653,7 +765,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     mbar_init(smem_u32(&sm.ifull[0]), 1);
     mbar_init(smem_u32(&sm.ifull[1]), 1);
     mbar_init(smem_u32(&sm.pitem), AT_PRODUCERS);
-    if (KV8)
+    if (FMT != kFmtBf16)
       for (int st = 0; st < AT_STAGES; ++st) mbar_init(smem_u32(&sm.rawf[st]), AT_PRODUCERS);
     sm.abort = 0;
     fence_barrier_init();
@@ -667,7 +779,7 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
   __syncthreads();
   grid_dep_wait();  // set-up above touches no global memory
   if (threadIdx.x >= AT_CONSUMERS)
-    attn_producer<KV8, SEGS>(sm, a, sg);
+    attn_producer<FMT, ADDR>(sm, a, sg);
   else
     attn_consumer(sm, a);
   __syncthreads();
@@ -777,15 +889,15 @@ size_t attn_mla_ws_bytes(int batch, int rows, int k) {
   return static_cast<size_t>(items) * p.maxp * AT_H * (AT_DV + 2) * sizeof(float);
 }
 
-template <bool KV8, bool SEGS>
-static ic_status launch_attn_inst(const AttnArgs& a, const AttnSegParam<SEGS>& sg, long grid,
+template <int FMT, int ADDR>
+static ic_status launch_attn_inst(const AttnArgs& a, const AttnAddrParam<ADDR>& sg, long grid,
                                   cudaStream_t stream) {
   const int smem = static_cast<int>(sizeof(AttnSmem)) + 128;
-  ic_status st = cuda_check(cudaFuncSetAttribute(attn_mla_kernel<KV8, SEGS>,
+  ic_status st = cuda_check(cudaFuncSetAttribute(attn_mla_kernel<FMT, ADDR>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                             "cudaFuncSetAttribute(attn)");
   if (st) return st;
-  return cuda_check(launch_dep(attn_mla_kernel<KV8, SEGS>, dim3(static_cast<unsigned>(grid)),
+  return cuda_check(launch_dep(attn_mla_kernel<FMT, ADDR>, dim3(static_cast<unsigned>(grid)),
                                dim3(AT_THREADS), smem, stream, 1, a, sg),
                     "attn_mla_kernel launch");
 }
@@ -793,7 +905,7 @@ static ic_status launch_attn_inst(const AttnArgs& a, const AttnSegParam<SEGS>& s
 ic_status launch_attn_mla(const void* q, const void* kv, long ld_kv, const int* idx, int batch,
                           int rows, int Lkv, int k, float scale, void* out, float* lse, void* ws,
                           size_t ws_bytes, long long valid_entries, cudaStream_t stream,
-                          bool kv8, const AttnSeg* segs, int nseg) {
+                          int fmt, const AttnSeg* segs, int nseg, const PagedArgs* pages) {
   const long items = static_cast<long>(batch) * rows;
   if (nseg < 0 || nseg > IC_MAXSEG || (nseg > 0 && (batch != 1 || !segs)))
     return fail(IC_ERR_INVALID_ARG, "attn: bad segment list (%d)", nseg);
@@ -825,24 +937,29 @@ ic_status launch_attn_mla(const void* q, const void* kv, long ld_kv, const int* 
   a.part_ml = p.split ? static_cast<float*>(ws) + items * p.maxp * AT_H * AT_DV : nullptr;
   const long grid = p.split ? p.G : (items < num_sms() ? items : num_sms());
   ic_status st;
-  if (nseg > 0) {
+  if (pages) {
+    st = fmt == kFmtMxf4   ? launch_attn_inst<kFmtMxf4, kAddrPaged>(a, *pages, grid, stream)
+         : fmt == kFmtE4m3 ? launch_attn_inst<kFmtE4m3, kAddrPaged>(a, *pages, grid, stream)
+                           : launch_attn_inst<kFmtBf16, kAddrPaged>(a, *pages, grid, stream);
+  } else if (nseg > 0) {
     AttnSegs sg;
     sg.nseg = nseg;
     for (int j = 0; j < nseg; ++j) sg.seg[j] = segs[j];
-    st = kv8 ? launch_attn_inst<true, true>(a, sg, grid, stream)
-             : launch_attn_inst<false, true>(a, sg, grid, stream);
+    st = fmt == kFmtE4m3 ? launch_attn_inst<kFmtE4m3, kAddrSegs>(a, sg, grid, stream)
+                         : launch_attn_inst<kFmtBf16, kAddrSegs>(a, sg, grid, stream);
   } else {
     const AttnNoSegs sg{0};
-    st = kv8 ? launch_attn_inst<true, false>(a, sg, grid, stream)
-             : launch_attn_inst<false, false>(a, sg, grid, stream);
+    st = fmt == kFmtE4m3 ? launch_attn_inst<kFmtE4m3, kAddrDense>(a, sg, grid, stream)
+                         : launch_attn_inst<kFmtBf16, kAddrDense>(a, sg, grid, stream);
   }
   if (st) return st;
   // algorithmic bytes: each selected latent row gathered once, q read once, out written once
   const double ve = valid_entries >= 0 ? static_cast<double>(valid_entries)
                                        : static_cast<double>(items) * k;
   const double io = static_cast<double>(items) * AT_H * (AT_DK + AT_DV) * 2.0;
-  trace_launch(kv8 ? kKindAttnMlaKv8 : kKindAttnMla, stream,
-               ve * (kv8 ? KV8_ROW_BYTES : AT_DK * 2.0) + io + 4.0 * static_cast<double>(items) * k);
+  const double row_b = fmt == kFmtMxf4 ? KV4_ROW_BYTES : fmt == kFmtE4m3 ? KV8_ROW_BYTES : AT_DK * 2;
+  trace_launch(fmt == kFmtMxf4 ? kKindAttnMlaKv4 : fmt == kFmtE4m3 ? kKindAttnMlaKv8 : kKindAttnMla,
+               stream, ve * row_b + io + 4.0 * static_cast<double>(items) * k);
   if (!p.split) return IC_OK;
   static_assert(AT_DV == 4 * 128, "combine: 128 threads x 4 dims");
   st = cuda_check(launch_dep(attn_combine_kernel, dim3(static_cast<unsigned>(items), AT_H), dim3(128),
@@ -860,6 +977,8 @@ ic_status launch_attn_mla(const void* q, const void* kv, long ld_kv, const int* 
 // ------------------------------------------------------------------ fp32 (MQA) form
 // One CTA per query row, CUDA cores: small shapes only (the fp32 workload has
 // 4 heads of dim 64 over k = 64 keys).
+template <bool SEGS>
+using AttnSegParam = AttnAddrParam<SEGS ? kAddrSegs : kAddrDense>;
 template <bool SEGS>
 __global__ void attn_f32_kernel(const float* q, const float* kv, long ld_kv, const float* v,
                                 const int* idx, int R, int heads, int dk, int dv, int Lkv_, int k,

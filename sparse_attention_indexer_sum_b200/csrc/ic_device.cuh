@@ -9,6 +9,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -37,6 +38,8 @@ enum DevErr : int {
   kErrBoundsTma = 17,     // a TMA tile coordinate outside its tensor's rows
   kErrBoundsTopk = 18,    // a top-k output slot or index outside its row
   kErrBoundsMerge = 19,   // a merge output slot or piece count out of range
+  kErrBoundsPage = 20,    // a page number outside the pool
+  kErrBoundsSlot = 21,    // a cache slot or position outside its cache or table
 };
 
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error, 0, code); }
@@ -283,6 +286,11 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 // row are equal.
 __device__ __forceinline__ uint64_t select_key(float score, uint32_t index) {
   return (static_cast<uint64_t>(score_key(score)) << 32) | static_cast<uint64_t>(~index);
+}
+
+// The power of two that an e8m0 code stands for (2^(code - 127); 255: NaN).
+__device__ __forceinline__ float e8m0_value(unsigned code) {
+  return __uint_as_float(code == 0u ? 0x00400000u : code == 255u ? 0x7FFFFFFFu : code << 23);
 }
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }

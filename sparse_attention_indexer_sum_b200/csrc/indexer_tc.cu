@@ -61,7 +61,13 @@ struct IdxTcArgs {
   // qb0 .. qb0 + ceil(R / TPM) - 1.  Used by the multi-token instances only.
   int nseg;
   IdxSeg seg[IC_MAXSEG];
+  // Pages (one query per sequence): sequence b's key s is row page << shift plus its
+  // place in the page; Lk bounds every length, and R, pos0, total_tiles are unused.
+  PagedArgs pg;
 };
+
+// How a query block's keys are found: a uniform batch, packed segments, or pages.
+constexpr int kIdxUniform = 0, kIdxSegs = 1, kIdxPaged = 2;
 
 // Fused top-k slot: a 64-byte header {int count; int pad; uint64 tau; uint64 max}
 // and then `count` selection keys (select_key) of one row's keys in one CTA:
@@ -158,10 +164,20 @@ struct QbInfo {
   long qrow0, krow0, orow0, pos0;
   int R, Lk, ql;
 };
-template <int TPM, bool SEGS>
+template <int TPM, int MODE>
 __host__ __device__ __forceinline__ QbInfo qb_info(const IdxTcArgs& a, int qb) {
   QbInfo x;
-  if (SEGS) {
+  if constexpr (MODE == kIdxPaged) {  // one query at the sequence's last token
+    x.ql = 0;
+    x.qrow0 = qb;
+    x.orow0 = qb;
+    x.krow0 = 0;
+    int n = a.pg.seq_lens[qb];
+    n = n < 0 ? 0 : n;
+    x.Lk = n < a.Lk ? n : a.Lk;
+    x.pos0 = x.Lk - 1;
+    x.R = 1;
+  } else if (MODE == kIdxSegs) {
     int lo = 0, hi = a.nseg - 1;  // the last segment with qb0 <= qb
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -191,23 +207,26 @@ __host__ __device__ __forceinline__ QbInfo qb_info(const IdxTcArgs& a, int qb) {
   return x;
 }
 
-template <int TPM, bool SEGS>
+template <int TPM, int MODE>
 __host__ __device__ __forceinline__ int qb_tiles(const IdxTcArgs& a, int qb) {
-  const QbInfo x = qb_info<TPM, SEGS>(a, qb);
+  const QbInfo x = qb_info<TPM, MODE>(a, qb);
   const int r_last = min(x.ql * TPM + TPM, x.R) - 1;
   long keys = x.pos0 + r_last + 1;
   if (keys > x.Lk) keys = x.Lk;
   return static_cast<int>((keys + 127) / 128);
 }
 
-template <int TPM, bool SEGS>
+template <int TPM, int MODE>
 struct WorkIt {
   int qb, kt, nt;
   __device__ __forceinline__ void advance(const IdxTcArgs& a) {
     if (++kt >= nt) {
       kt = 0;
       ++qb;
-      nt = (qb < a.nqb) ? qb_tiles<TPM, SEGS>(a, qb) : 0;
+      nt = (qb < a.nqb) ? qb_tiles<TPM, MODE>(a, qb) : 0;
+      if constexpr (MODE == kIdxPaged) {  // empty sequences have no tiles
+        while (nt == 0 && qb + 1 < a.nqb) nt = qb_tiles<TPM, MODE>(a, ++qb);
+      }
     }
   }
 };
@@ -386,7 +405,7 @@ __device__ __noinline__ CompactResult cand_compact(CandSet cs, const int cnt, ui
   return r;
 }
 
-template <bool FP8, int TPM, bool FUSED, bool SEGS>
+template <bool FP8, int TPM, bool FUSED, int MODE>
 __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
     indexer_tc_kernel(const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ IdxTcArgs a) {
@@ -422,9 +441,11 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
   const uint32_t a_base = smem_u32(smem + C::OFF_A);
   const uint32_t q_base = smem_u32(smem + C::OFF_Q);
 
-  const long g0 = a.total_tiles * blockIdx.x / gridDim.x;
-  const long g1 = a.total_tiles * (blockIdx.x + 1) / gridDim.x;
-  const long nitems = g1 - g0;
+  // paged: the tiles are counted on the device, from the lengths there
+  long* total_smem = reinterpret_cast<long*>(smem + C::OFF_MISC + 16);
+  static_assert(MODE != kIdxPaged || (!FUSED && TPM == 1), "pages: one query per sequence");
+  long g0 = a.total_tiles * blockIdx.x / gridDim.x;
+  long g1 = a.total_tiles * (blockIdx.x + 1) / gridDim.x;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -455,11 +476,21 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmQ);
     }
+    if constexpr (MODE == kIdxPaged) {
+      grid_dep_wait();
+      __syncwarp();
+      long t = 0;
+      for (int qb = lane; qb < a.nqb; qb += 32) t += qb_tiles<TPM, MODE>(a, qb);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane == 0) *total_smem = t;
+      g0 = t * blockIdx.x / gridDim.x;
+    }
     // Locate tile g0 in the (query block, key tile) list: warp-parallel prefix scan.
     long cum = 0;
     for (int base = 0; base < a.nqb; base += 32) {
       const int qb = base + lane;
-      const long t = (qb < a.nqb) ? qb_tiles<TPM, SEGS>(a, qb) : 0;
+      const long t = (qb < a.nqb) ? qb_tiles<TPM, MODE>(a, qb) : 0;
       long incl = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -488,13 +519,97 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  grid_dep_wait();  // set-up above touches no global memory
+  grid_dep_wait();  // set-up above touches no global memory (pages: warp 0 has waited)
+  if constexpr (MODE == kIdxPaged) {
+    const long total = *total_smem;
+    g0 = total * blockIdx.x / gridDim.x;
+    g1 = total * (blockIdx.x + 1) / gridDim.x;
+  }
+  const long nitems = g1 - g0;
 
   if (nitems > 0) {
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
-      if (lane == 0) {
-        WorkIt<TPM, SEGS> it{start[0], start[1], qb_tiles<TPM, SEGS>(a, start[0])};
+      if constexpr (MODE == kIdxPaged) {
+        // The whole warp walks the tiles: lane l holds the numbers of pages base + l
+        // and base + 32 + l of the sequence (the second set is fetched 32 pages
+        // ahead, so no tile waits for the page table), lane 0 issues the copies, one
+        // per page or per 128 rows.  Rows past the sequence's end are not copied.
+        // A page number outside the pool reads as zeros (out of the map's bounds).
+        WorkIt<TPM, MODE> it{start[0], start[1], qb_tiles<TPM, MODE>(a, start[0])};
+        const int ps = 1 << a.pg.shift;
+        const int per = ps < C::BM ? C::BM >> a.pg.shift : 1;  // copies of a whole tile
+        const int rows = ps < C::BM ? ps : C::BM;              // rows of each
+        const int oob = a.pg.num_pages << a.pg.shift;
+        int stage = 0, cur_qb = -1, qloads = 0, base = 0, len = 0;
+        int cur = 0, nxt = 0;
+        uint32_t ph = 0;
+        long issued = 0;
+        auto fetch = [&](int qb, int p) -> int {
+          const int e = (static_cast<long>(p) << a.pg.shift) < len ? a.pg.table[qb * a.pg.ld_table + p] : -1;
+          return e >= 0 && e < a.pg.num_pages ? e : -1;
+        };
+        for (long i = 0; i < nitems; ++i) {
+          const int p0 = (it.kt * C::BM) >> a.pg.shift;
+          if (it.qb != cur_qb) {
+            len = qb_info<TPM, MODE>(a, it.qb).Lk;
+            base = p0 & ~31;
+            cur = fetch(it.qb, base + lane);
+            nxt = fetch(it.qb, base + 32 + lane);
+            if (!__all_sync(0xffffffffu, qloads == 0 || mbar_wait(qempty_bar, (qloads - 1) & 1,
+                                                                  abort_flag, kErrTimeoutProducer)))
+              break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(qfull_bar, C::Q_BYTES);
+#pragma unroll
+              for (int kb = 0; kb < C::KBLK; ++kb)
+                tma_load_2d(q_base + kb * (C::N * 128), &tmQ, kb * C::ELEMS_128B, it.qb * 64,
+                            qfull_bar);
+            }
+            ++qloads;
+            cur_qb = it.qb;
+          } else if (p0 >= base + 32) {
+            base += 32;
+            cur = nxt;
+            nxt = fetch(it.qb, base + 32 + lane);
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), ph ^ 1, abort_flag,
+                                                 kErrTimeoutProducer)))
+            break;
+          const int left = len - it.kt * C::BM;
+          const int n = left >= C::BM ? per : (left + rows - 1) / rows;  // copies of this tile
+          if (lane == 0) mbar_arrive_expect_tx(full_bar(stage), n * rows * C::ROWB);
+          __syncwarp();
+          for (int j = 0; j < n; ++j) {
+            const int page = __shfl_sync(0xffffffffu, cur, (p0 + j) & 31);
+            const bool ok = in_bounds(page >= 0, kErrBoundsPage) && page >= 0;
+            const int krow =
+                ok ? (page << a.pg.shift) + ((it.kt * C::BM) & (ps - 1)) : oob;
+            if (lane == 0) {
+#pragma unroll
+              for (int kb = 0; kb < C::KBLK; ++kb)
+                tma_load_2d(a_base + stage * C::A_BYTES + kb * (C::BM * 128) + j * rows * 128,
+                            &tmK, kb * C::ELEMS_128B, krow, full_bar(stage));
+            }
+          }
+          ++issued;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            ph ^= 1;
+          }
+          it.advance(a);
+        }
+        if (*abort_flag && lane == 0) {
+          // let every copy started land before the CTA's smem goes away
+          long n = issued < C::STAGES ? issued : C::STAGES;
+          for (long j = issued - n; j < issued; ++j)
+            mbar_wait_drain(full_bar(static_cast<int>(j % C::STAGES)),
+                            static_cast<uint32_t>((j / C::STAGES) & 1));
+          if (qloads > 0) mbar_wait_drain(qfull_bar, (qloads - 1) & 1);
+        }
+        __syncwarp();
+      } else if (lane == 0) {
+        WorkIt<TPM, MODE> it{start[0], start[1], qb_tiles<TPM, MODE>(a, start[0])};
         int stage = 0;
         uint32_t ph = 0;
         int qloads = 0, cur_qb = -1;
@@ -504,7 +619,7 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
             if (qloads > 0 &&
                 !mbar_wait(qempty_bar, (qloads - 1) & 1, abort_flag, kErrTimeoutProducer))
               break;
-            const QbInfo x = qb_info<TPM, SEGS>(a, it.qb);
+            const QbInfo x = qb_info<TPM, MODE>(a, it.qb);
             const int qrow = static_cast<int>((x.qrow0 + x.ql * TPM) * 64);
             (void)in_bounds(qrow >= 0 && x.ql * TPM < x.R, kErrBoundsTma);  // loads stay legal
             mbar_arrive_expect_tx(qfull_bar, C::Q_BYTES);
@@ -515,7 +630,7 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
             cur_qb = it.qb;
           }
           if (!mbar_wait(empty_bar(stage), ph ^ 1, abort_flag, kErrTimeoutProducer)) break;
-          const QbInfo kx = qb_info<TPM, SEGS>(a, it.qb);
+          const QbInfo kx = qb_info<TPM, MODE>(a, it.qb);
           const int krow = static_cast<int>(kx.krow0 + it.kt * C::BM);
           (void)in_bounds(krow >= 0 && it.kt * C::BM < kx.Lk, kErrBoundsTma);
           mbar_arrive_expect_tx(full_bar(stage), C::A_BYTES);
@@ -554,7 +669,7 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
         for (int kk = 0; kk < C::KSTEPS; ++kk)
           bdesc[kk] = sdesc_k_sw128(q_base + (kk / 4) * (C::N * 128) + (kk % 4) * 32);
         const uint64_t adesc0 = sdesc_k_sw128(a_base);
-        WorkIt<TPM, SEGS> it{start[0], start[1], qb_tiles<TPM, SEGS>(a, start[0])};
+        WorkIt<TPM, MODE> it{start[0], start[1], qb_tiles<TPM, MODE>(a, start[0])};
         int stage = 0, acc = 0;
         uint32_t ph = 0, aph = 0;
         int qwaits = 0, cur_qb = -1;
@@ -581,7 +696,7 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
             tc_commit(empty_bar(stage));
             tc_commit(accfull_bar(acc));
           }
-          WorkIt<TPM, SEGS> nx = it;
+          WorkIt<TPM, MODE> nx = it;
           nx.advance(a);
           if (i + 1 == nitems || nx.qb != it.qb) tc_commit(qempty_bar);
           it = nx;
@@ -605,10 +720,11 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
       const int set = e / C::SETW;  // accumulator slots a with a % NSETS == set
       const int member = (e % C::SETW) / 4;  // which tokens of the block this warp reduces
       float* wsl = w_smem + e * C::TOK_PER_EW * 64;
-      WorkIt<TPM, SEGS> it{start[0], start[1], qb_tiles<TPM, SEGS>(a, start[0])};
+      WorkIt<TPM, MODE> it{start[0], start[1], qb_tiles<TPM, MODE>(a, start[0])};
       int acc = 0;
       uint32_t aph = 0;
       int cur_qb = -1;
+      QbInfo pq{};  // paged: the sequence's, read once per sequence
       // head weights of this warp's tokens: the warp's shared copy (wsl), written
       // when a query block starts; a warp with several tokens keeps them in registers
       // (wr), a one-token warp reads them with one broadcast load per 4 heads
@@ -629,7 +745,10 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
           it.advance(a);
           continue;
         }
-        const QbInfo qi = qb_info<TPM, SEGS>(a, it.qb);
+        if constexpr (MODE == kIdxPaged) {
+          if (it.qb != cur_qb) pq = qb_info<TPM, MODE>(a, it.qb);
+        }
+        const QbInfo qi = MODE == kIdxPaged ? pq : qb_info<TPM, MODE>(a, it.qb);
         const int r0 = qi.ql * TPM + member * C::TOK_PER_EW;
         if (it.qb != cur_qb) {
           __syncwarp();
@@ -657,7 +776,17 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
         const int s = it.kt * C::BM + qd * 32 + lane;
         const bool key_ok = s < qi.Lk;
         float ks = 1.f;
-        if constexpr (FP8) ks = key_ok ? a.k_scale[qi.krow0 + s] : 0.f;
+        if constexpr (FP8 && MODE == kIdxPaged) {
+          if (key_ok) {
+            const int page = __ldg(a.pg.table + it.qb * a.pg.ld_table + (s >> a.pg.shift));
+            ks = 0.f;
+            if (page >= 0 && page < a.pg.num_pages)
+              ks = a.k_scale[(static_cast<long>(page) << a.pg.shift) +
+                             (s & ((1 << a.pg.shift) - 1))];
+          }
+        } else if constexpr (FP8) {
+          ks = key_ok ? a.k_scale[qi.krow0 + s] : 0.f;
+        }
         // every lane leaves together, so the warp never splits before tcgen05.ld
         const bool acc_ok = __all_sync(0xffffffffu, mbar_wait(accfull_bar(acc), aph, abort_flag,
                                                               kErrTimeoutEpilogue));
@@ -819,7 +948,7 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
           const uint64_t* stg = reinterpret_cast<const uint64_t*>(smem + C::OFF_STG);
           const int* scnt = reinterpret_cast<const int*>(smem + C::OFF_SCNT);
           uint64_t* const cbuf = reinterpret_cast<uint64_t*>(smem + C::OFF_CBUF);
-          WorkIt<TPM, SEGS> it{start[0], start[1], qb_tiles<TPM, SEGS>(a, start[0])};
+          WorkIt<TPM, MODE> it{start[0], start[1], qb_tiles<TPM, MODE>(a, start[0])};
           int ccnt = 0, crow = -1;
           uint64_t ctau = 0, kmx = 0;  // kmx: this lane's largest appended key
           long crow_first = 0;         // first CTA of the current row
@@ -1030,7 +1159,7 @@ static ic_status launch_tpl(const void* q, const float* q_scale, const void* k,
   a.topk = topk;
   a.nseg = 0;
   long total = 0;
-  for (int qb = 0; qb < a.qb_per_batch; ++qb) total += qb_tiles<TPM, false>(a, qb);
+  for (int qb = 0; qb < a.qb_per_batch; ++qb) total += qb_tiles<TPM, kIdxUniform>(a, qb);
   total *= batch;  // every batch has the same triangle
   a.total_tiles = total;
   if (total == 0) return IC_OK;
@@ -1041,12 +1170,12 @@ static ic_status launch_tpl(const void* q, const float* q_scale, const void* k,
   st = make_map(&tmQ, q, FP8, static_cast<uint64_t>(batch) * rows * 64, C::N);
   if (st) return st;
 
-  st = cuda_check(cudaFuncSetAttribute(indexer_tc_kernel<FP8, TPM, FUSED, false>,
+  st = cuda_check(cudaFuncSetAttribute(indexer_tc_kernel<FP8, TPM, FUSED, kIdxUniform>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES),
                   "cudaFuncSetAttribute(indexer)");
   if (st) return st;
   const long grid = total < num_sms() ? total : num_sms();
-  st = cuda_check(launch_dep(indexer_tc_kernel<FP8, TPM, FUSED, false>, dim3(static_cast<unsigned>(grid)),
+  st = cuda_check(launch_dep(indexer_tc_kernel<FP8, TPM, FUSED, kIdxUniform>, dim3(static_cast<unsigned>(grid)),
                              dim3(C::THREADS), C::SMEM_BYTES, stream, 1, tmK, tmQ, a),
                   "indexer_tc_kernel launch");
   if (st) return st;
@@ -1091,7 +1220,7 @@ static ic_status launch_segs(const void* q, const float* q_scale, const void* k,
   }
   a.nqb = nqb;
   long total = 0;
-  for (int qb = 0; qb < nqb; ++qb) total += qb_tiles<TPM, true>(a, qb);
+  for (int qb = 0; qb < nqb; ++qb) total += qb_tiles<TPM, kIdxSegs>(a, qb);
   a.total_tiles = total;
   if (total == 0) return IC_OK;
 
@@ -1100,12 +1229,12 @@ static ic_status launch_segs(const void* q, const float* q_scale, const void* k,
   if (st) return st;
   st = make_map(&tmQ, q, FP8, static_cast<uint64_t>(q_rows) * 64, C::N);
   if (st) return st;
-  st = cuda_check(cudaFuncSetAttribute(indexer_tc_kernel<FP8, TPM, false, true>,
+  st = cuda_check(cudaFuncSetAttribute(indexer_tc_kernel<FP8, TPM, false, kIdxSegs>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES),
                   "cudaFuncSetAttribute(indexer)");
   if (st) return st;
   const long grid = total < num_sms() ? total : num_sms();
-  st = cuda_check(launch_dep(indexer_tc_kernel<FP8, TPM, false, true>, dim3(static_cast<unsigned>(grid)),
+  st = cuda_check(launch_dep(indexer_tc_kernel<FP8, TPM, false, kIdxSegs>, dim3(static_cast<unsigned>(grid)),
                              dim3(C::THREADS), C::SMEM_BYTES, stream, 1, tmK, tmQ, a),
                   "indexer_tc_kernel launch");
   if (st) return st;
@@ -1122,6 +1251,63 @@ ic_status launch_indexer_tc_segs(bool fp8, const void* q, const float* q_scale, 
                                  stream)
              : launch_segs<false>(q, q_scale, k, k_scale, w, segs, nseg, q_rows, k_rows, scores,
                                   ld, stream);
+}
+
+// One query per sequence over paged keys (see IdxTcArgs::pg): every sequence's tiles
+// are counted on the device, so the lengths may change between two replays of a graph.
+template <bool FP8>
+static ic_status launch_paged(const void* q, const float* q_scale, const void* k,
+                              const float* k_scale, const float* w, int batch,
+                              const PagedArgs& pg, float* scores, long ld, cudaStream_t stream) {
+  using C = IdxCfg<FP8, 1, false>;
+  IdxTcArgs a;
+  a.w = w;
+  a.q_scale = q_scale;
+  a.k_scale = k_scale;
+  a.scores = scores;
+  a.ld = ld;
+  a.B = batch;
+  a.R = 1;
+  a.Lk = pg.max_len;
+  a.pos0 = 0;
+  a.qb_per_batch = 1;
+  a.nqb = batch;
+  a.cslots = nullptr;
+  a.maxp = 0;
+  a.topk = 0;
+  a.nseg = 0;
+  a.pg = pg;
+  a.total_tiles = 0;
+  const long most = static_cast<long>(batch) * ((pg.max_len + 127) / 128);
+  CUtensorMap tmK, tmQ;
+  const int ps = 1 << pg.shift;
+  ic_status st = make_map(&tmK, k, FP8, static_cast<uint64_t>(pg.num_pages) << pg.shift,
+                          static_cast<uint32_t>(ps < C::BM ? ps : C::BM));
+  if (st) return st;
+  st = make_map(&tmQ, q, FP8, static_cast<uint64_t>(batch) * 64, C::N);
+  if (st) return st;
+  st = cuda_check(cudaFuncSetAttribute(indexer_tc_kernel<FP8, 1, false, kIdxPaged>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES),
+                  "cudaFuncSetAttribute(indexer)");
+  if (st) return st;
+  const long grid = most < num_sms() ? most : num_sms();
+  st = cuda_check(launch_dep(indexer_tc_kernel<FP8, 1, false, kIdxPaged>,
+                             dim3(static_cast<unsigned>(grid)), dim3(C::THREADS), C::SMEM_BYTES,
+                             stream, 1, tmK, tmQ, a),
+                  "indexer_tc_kernel launch");
+  if (st) return st;
+  // the lengths are on the device: the work of full ones is reported
+  trace_launch(FP8 ? kKindIndexerE4m3 : kKindIndexerBf16, stream,
+               2.0 * 64 * 128 * static_cast<double>(batch) * pg.max_len);
+  return IC_OK;
+}
+
+ic_status launch_indexer_tc_paged(bool fp8, const void* q, const float* q_scale, const void* k,
+                                  const float* k_scale, const float* w, int batch,
+                                  const PagedArgs& pg, float* scores, long ld,
+                                  cudaStream_t stream) {
+  return fp8 ? launch_paged<true>(q, q_scale, k, k_scale, w, batch, pg, scores, ld, stream)
+             : launch_paged<false>(q, q_scale, k, k_scale, w, batch, pg, scores, ld, stream);
 }
 
 // Plan of the fused indexer -> top-k for `batch` sequences of one query each at

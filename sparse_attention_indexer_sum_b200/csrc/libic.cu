@@ -4,5 +4,6 @@
 #include "topk.cu"
 #include "attn.cu"
 #include "misc.cu"
+#include "cache.cu"
 #include "api.cu"
 #include "noalloc.cu"

@@ -124,7 +124,7 @@ ic_status ic_sparse_attn_noalloc(const void* q, const void* kv, long ld_kv, cons
   // previous call's contents need no clearing.
   return launch_attn_mla(q, kv, ld_kv, idx, batch, rows, Lkv, k, scale, out, lse, scratch,
                          IC_NOALLOC_SCRATCH_BYTES, -1, static_cast<cudaStream_t>(stream),
-                         dt == IC_E4M3);
+                         dt == IC_E4M3 ? kFmtE4m3 : kFmtBf16);
 }
 
 }  // extern "C"
