@@ -458,79 +458,127 @@ def decode_step_graph(pattern: str, desc: ic_stack_desc, layers: list[dict], t_c
 
 
 # ------------------------------------------------------------------ around the path
+# These wrappers also run for single tokens, where the host's time per call counts: they
+# read each tensor's properties once and pass pointers as plain integers.
 KV4_ROW_BYTES = 400
 _DT = {torch.float32: IC_F32, torch.bfloat16: IC_BF16}
 _KV_ROW = {IC_BF16: 2 * 576, IC_E4M3: KV8_ROW_BYTES, IC_MXF4: KV4_ROW_BYTES}
 
 
-def _one_device(*ts):
-    """The CUDA device that every given tensor lives on (a ValueError otherwise)."""
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _one_device(*ts) -> int:
+    """The index of the CUDA device that every given tensor lives on (else a ValueError)."""
     dev = None
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device (got one on %s)" % t.device)
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors are on %s and %s" % (dev, t.device))
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("tensors must be on a CUDA device (got one on %s)" % t.device)
+                if dev is not None:
+                    raise ValueError("tensors are on cuda:%d and cuda:%d" % (dev, d))
+                dev = d
     return dev
 
 
 class _On:
-    """Runs the body with `dev` current and allocations made for `stream`; yields the raw stream."""
+    """Makes device `dev` current and `stream` the one that allocations are made for; yields
+    the raw stream to launch on."""
 
-    def __init__(self, dev, stream):
+    def __init__(self, dev: int, stream):
         self.dev, self.stream, self.held = dev, stream, []
 
     def __enter__(self):
-        if self.dev.index != torch.cuda.current_device():
+        if self.dev != torch.cuda.current_device():
             self.held.append(torch.cuda.device(self.dev))
             self.held[-1].__enter__()
-        if self.stream is not None:
-            s = self.stream
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s), device=self.dev)
-            elif s.device != self.dev:
-                self.__exit__(None, None, None)
-                raise ValueError("stream of %s, tensors on %s" % (s.device, self.dev))
-            self.held.append(torch.cuda.stream(s))
-            self.held[-1].__enter__()
-        return _stream(self.stream)
+        s = self.stream
+        if s is None:
+            return torch.cuda.current_stream().cuda_stream
+        if not isinstance(s, torch.cuda.Stream):
+            s = torch.cuda.ExternalStream(int(s), device=self.dev)
+        elif s.device.index != self.dev:
+            self.__exit__(None, None, None)
+            raise ValueError("stream of %s, tensors on cuda:%d" % (s.device, self.dev))
+        self.held.append(torch.cuda.stream(s))
+        self.held[-1].__enter__()
+        return s.cuda_stream
 
     def __exit__(self, *exc):
         while self.held:
             self.held.pop().__exit__(*exc)
 
 
-def _rows2d(t, name, n, dtypes):
-    """(rows, row stride) of t [..., n] whose leading dims are dense over the row stride."""
-    if t.dtype not in dtypes or t.dim() < 1 or t.shape[-1] != n:
-        raise ValueError("%s must be %s [..., %d]" % (name, " or ".join(map(str, dtypes)), n))
-    if n > 1 and t.stride(-1) != 1:
+def _rows2d(t, name, n, dtype):
+    """(rows, row stride) of t [..., n] whose leading dims are evenly spaced."""
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s" % (name, dtype))
+    shape = t.shape
+    if not shape or shape[-1] != n:
+        raise ValueError("%s must be [..., %d]" % (name, n))
+    if t.is_contiguous():
+        return t.numel() // n if n else 0, n
+    stride = t.stride()
+    if n > 1 and stride[-1] != 1:
         raise ValueError("%s rows must be contiguous" % name)
     rows, ld = 1, None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if size != 1:
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] != 1:
             if ld is None:
-                ld = stride
-            elif stride != ld * rows:
+                ld = stride[i]
+            elif stride[i] != ld * rows:
                 raise ValueError("%s rows must be evenly spaced" % name)
-            rows *= size
+            rows *= shape[i]
     return rows, n if ld is None else ld
 
 
-def _pool(t, name, dtypes, row_bytes=0):
-    """(slots, row stride in elements, row length) of a cache [slots, w] or [pages, page, w]."""
-    if t.dim() not in (2, 3) or t.dtype not in dtypes:
-        raise ValueError("%s must be %s [slots, width] or [pages, page_size, width]" % (
-            name, " or ".join(map(str, dtypes))))
+def _like(t, name, shape, dtype):
+    """The row stride of t, which has the given shape."""
+    if t.shape != shape:
+        raise ValueError("%s must have x's shape" % name)
+    return _rows2d(t, name, shape[-1], dtype)[1]
+
+
+def _pool(t, name, dtype, row_bytes=0):
+    """(slots, row stride in elements) of a cache [slots, w] or [pages, page_size, w]."""
+    if t.dim() not in (2, 3):
+        raise ValueError("%s must be [slots, width] or [pages, page_size, width]" % name)
     w = t.shape[-1]
     if w * t.element_size() < row_bytes:
         raise ValueError("%s rows must hold %d bytes" % (name, row_bytes))
-    rows, ld = _rows2d(t, name, w, dtypes)
-    return rows, ld, w
+    return _rows2d(t, name, w, dtype)
+
+
+def _kv_pool(kv_cache, kv_dtype):
+    if kv_dtype is None and kv_cache.dtype == torch.bfloat16:
+        kv_dtype = IC_BF16
+    if kv_dtype not in _KV_ROW:
+        raise ValueError("kv_dtype must be IC_BF16, IC_E4M3 or IC_MXF4")
+    slots, ld = _pool(kv_cache, "kv_cache", torch.bfloat16 if kv_dtype == IC_BF16 else torch.uint8,
+                      _KV_ROW[kv_dtype])
+    return kv_dtype, slots, ld
+
+
+def _launch(dev, stream, call):
+    """call(raw stream) with `dev` current; its status is checked."""
+    if stream is None and dev == torch.cuda.current_device():
+        st = call(torch._C._cuda_getCurrentRawStream(dev))  # a tenth of current_stream()'s time
+    else:
+        with _On(dev, stream) as raw:
+            st = call(raw)
+    if st != IC_OK:
+        raise ICError(st, ic_last_error())
+
+
+def _new(shape, dtype, dev, stream):
+    """A new tensor on device `dev`, allocated for `stream`."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    with _On(dev, stream):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
 
 
 def ic_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, h=None, y=None, codes=None,
@@ -538,29 +586,34 @@ def ic_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, h=None, y=None, 
     """RMS norm of x [..., n] (+ residual): h = x + residual, y = h / sqrt(mean h^2 + eps) *
     weight.  Writes the outputs that are given (h, y like x; codes uint8 [..., n] with
     scales f32 [..., ceil(n / 128)]), or a new y if none is; returns (y, codes, scales)."""
-    n = x.shape[-1]
-    rows, ld_x = _rows2d(x, "x", n, (torch.bfloat16, torch.float32))
-    if weight.dtype not in _DT or tuple(weight.shape) != (n,) or not weight.is_contiguous():
+    dt, shape = x.dtype, x.shape
+    if dt not in _DT or not shape:
+        raise ValueError("x must be bf16 or fp32 [..., n]")
+    n = shape[-1]
+    rows, ld_x = _rows2d(x, "x", n, dt)
+    if weight.dtype not in _DT or weight.dim() != 1 or weight.shape[0] != n or \
+            not weight.is_contiguous():
         raise ValueError("weight must be bf16 or fp32 [%d], contiguous" % n)
     dev = _one_device(x, weight, residual, h, y, codes, scales)
-    with _On(dev, stream) as st:
-        if h is None and y is None and codes is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        lds = []
-        for t, name, dt in ((residual, "residual", x.dtype), (h, "h", x.dtype), (y, "y", x.dtype),
-                            (codes, "codes", torch.uint8)):
-            if t is not None and t.shape != x.shape:
-                raise ValueError("%s must have x's shape" % name)
-            lds.append(0 if t is None else _rows2d(t, name, n, (dt,))[1])
-        if (codes is None) != (scales is None):
-            raise ValueError("codes and scales go together")
-        if scales is not None and (scales.dtype != torch.float32 or not scales.is_contiguous() or
-                                   tuple(scales.shape) != tuple(x.shape[:-1]) + (-(-n // 128),)):
-            raise ValueError("scales must be fp32 %s, contiguous" %
-                             (tuple(x.shape[:-1]) + (-(-n // 128),),))
-        _check(lib().ic_rms_norm(_p(x), ld_x, _p(residual), lds[0], _DT[x.dtype], _p(weight),
-                                 _DT[weight.dtype], float(eps), rows, n, _p(h), lds[1], _p(y),
-                                 lds[2], _p(codes), lds[3], _p(scales), st))
+    if h is None and y is None and codes is None:
+        y = _new(shape, dt, dev, stream)
+    ld_r = ld_h = ld_y = ld_c = 0
+    if residual is not None:
+        ld_r = _like(residual, "residual", shape, dt)
+    if h is not None:
+        ld_h = _like(h, "h", shape, dt)
+    if y is not None:
+        ld_y = _like(y, "y", shape, dt)
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales go together")
+    if codes is not None:
+        ld_c = _like(codes, "codes", shape, torch.uint8)
+        if scales.dtype != torch.float32 or not scales.is_contiguous() or \
+                scales.shape != shape[:-1] + (-(-n // 128),):
+            raise ValueError("scales must be fp32 [..., %d], contiguous" % -(-n // 128))
+    _launch(dev, stream, lambda st: lib().ic_rms_norm(
+        x.data_ptr(), ld_x, _ptr(residual), ld_r, _DT[dt], weight.data_ptr(), _DT[weight.dtype],
+        eps, rows, n, _ptr(h), ld_h, _ptr(y), ld_y, _ptr(codes), ld_c, _ptr(scales), st))
     return y, codes, scales
 
 
@@ -589,60 +642,65 @@ def ic_cache_append(slots, *, kv=None, kv_cache=None, kv_dtype=None, k=None, k_c
         raise ValueError("nothing to append")
     if (rope is None) != (pos is None):
         raise ValueError("rope goes with pos")
+    rope_rows = 0
     if rope is not None:
         if rope.dtype != torch.float32 or rope.dim() != 2 or rope.shape[1] != 64 or \
                 not rope.is_contiguous():
             raise ValueError("rope must be fp32 [positions, 64], contiguous")
-        if pos.dtype != torch.int32 or tuple(pos.shape) != (rows,) or not pos.is_contiguous():
+        if pos.dtype != torch.int32 or pos.dim() != 1 or pos.shape[0] != rows or \
+                not pos.is_contiguous():
             raise ValueError("pos must be int32 [rows], contiguous")
-    sizes, ld_kv, ld_cache, ld_k, k_dt = set(), 0, 0, 0, IC_BF16
+        rope_rows = rope.shape[0]
+    count = None
+    ld_kv = ld_cache = ld_k = 0
+    k_dt = IC_BF16
     if kv is not None:
-        if kv_dtype is None:
-            kv_dtype = IC_BF16 if kv_cache.dtype == torch.bfloat16 else None
-        if kv_dtype not in (IC_BF16, IC_E4M3, IC_MXF4):
-            raise ValueError("kv_dtype must be IC_BF16, IC_E4M3 or IC_MXF4")
-        n, ld_kv = _rows2d(kv, "kv", 576, (torch.bfloat16,))
-        slot_count, ld_cache, _ = _pool(kv_cache, "kv_cache", (
-            torch.bfloat16 if kv_dtype == IC_BF16 else torch.uint8,), _KV_ROW[kv_dtype])
+        n, ld_kv = _rows2d(kv, "kv", 576, torch.bfloat16)
+        kv_dtype, count, ld_cache = _kv_pool(kv_cache, kv_dtype)
         if n != rows:
             raise ValueError("kv must have %d rows" % rows)
-        sizes.add(slot_count)
+    else:
+        kv_dtype = IC_BF16
     if k is not None:
-        n, ld_k = _rows2d(k, "k", 128, (torch.bfloat16,))
-        slot_count, ld, w = _pool(k_cache, "k_cache", (torch.bfloat16, torch.uint8))
-        if n != rows or w != 128 or ld != 128:
-            raise ValueError("k must have %d rows, k_cache dense rows of 128" % rows)
-        sizes.add(slot_count)
+        n, ld_k = _rows2d(k, "k", 128, torch.bfloat16)
         if k_cache.dtype == torch.uint8:
             k_dt = IC_E4M3
-            if k_scale is None or k_scale.dtype != torch.float32 or \
-                    k_scale.numel() != slot_count or not k_scale.is_contiguous():
-                raise ValueError("an e4m3 key cache needs k_scale, fp32, one per slot")
-    if len(sizes) != 1:
-        raise ValueError("kv_cache and k_cache differ in their number of slots")
+        elif k_cache.dtype != torch.bfloat16:
+            raise ValueError("k_cache must be bf16 or uint8")
+        key_slots, ld = _pool(k_cache, "k_cache", k_cache.dtype)
+        if n != rows or ld != 128 or k_cache.shape[-1] != 128:
+            raise ValueError("k must have %d rows, k_cache dense rows of 128" % rows)
+        if count is not None and key_slots != count:
+            raise ValueError("kv_cache and k_cache differ in their number of slots")
+        count = key_slots
+        if k_dt == IC_E4M3 and (k_scale is None or k_scale.dtype != torch.float32 or
+                                k_scale.numel() != count or not k_scale.is_contiguous()):
+            raise ValueError("an e4m3 key cache needs k_scale, fp32, one per slot")
     if rows == 0:
         return
-    with _On(dev, stream) as st:
-        _check(lib().ic_cache_append(
-            rows, _p(slots), _p(pos), _p(rope), 0 if rope is None else rope.shape[0], _p(kv),
-            ld_kv, _p(kv_cache), ld_cache, IC_BF16 if kv_dtype is None else kv_dtype, _p(k), ld_k,
-            _p(k_cache), _p(k_scale) if k_dt == IC_E4M3 else None, k_dt, sizes.pop(),
-            (IC_ROPE_KV_HALVES if kv_halves else 0) | (IC_ROPE_K_HALVES if k_halves else 0), st))
+    flags = (IC_ROPE_KV_HALVES if kv_halves else 0) | (IC_ROPE_K_HALVES if k_halves else 0)
+    _launch(dev, stream, lambda st: lib().ic_cache_append(
+        rows, slots.data_ptr(), _ptr(pos), _ptr(rope), rope_rows, _ptr(kv), ld_kv, _ptr(kv_cache),
+        ld_cache, kv_dtype, _ptr(k), ld_k, _ptr(k_cache),
+        k_scale.data_ptr() if k_dt == IC_E4M3 else None, k_dt, count, flags, st))
 
 
 def make_paging(block_table, seq_lens, page_size: int, num_pages: int) -> ic_paging:
     """ic_paging over block_table [batch, max_pages] int32 and seq_lens [batch] int32 (device
     tensors that the caller keeps alive)."""
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [batch, max_pages] with contiguous rows")
-    if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (block_table.shape[0],) or \
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [batch, max_pages]")
+    batch, cols = block_table.shape
+    ld = cols
+    if not block_table.is_contiguous():
+        if cols > 1 and block_table.stride(1) != 1:
+            raise ValueError("block_table must have contiguous rows")
+        if batch > 1:
+            ld = block_table.stride(0)
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] != batch or \
             not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be int32 [batch], contiguous")
-    ld = block_table.stride(0) if block_table.shape[0] > 1 else block_table.shape[1]
-    return ic_paging(block_table=block_table.data_ptr(), ld_table=ld,
-                     max_pages=block_table.shape[1], seq_lens=seq_lens.data_ptr(),
-                     page_size=int(page_size), num_pages=int(num_pages))
+    return ic_paging(block_table.data_ptr(), ld, cols, seq_lens.data_ptr(), page_size, num_pages)
 
 
 def _pages(rows, page_size, name):
@@ -657,33 +715,42 @@ def ic_indexer_scores_paged(q, k_cache, w, block_table, seq_lens, *, page_size: 
     q [B, 64, 128] or [B, 1, 64, 128], w [B(, 1), 64], k_cache [slots, 128] or [pages, page_size,
     128] (bf16, or uint8 e4m3 codes with q_scale [B(, 1), 64] and k_scale, one per slot).
     Writes columns s < seq_lens[b] of `scores` (new: [B, max_pages * page_size]) only."""
-    _contig(q, w, q_scale, k_scale)
-    slots, ld, d = _pool(k_cache, "k_cache", (torch.bfloat16, torch.uint8))
-    B = block_table.shape[0]
-    H = q.shape[-2]
-    if q.dtype != k_cache.dtype or d != q.shape[-1] or ld != d:
-        raise ValueError("q and k_cache must have one type and dense rows of one length")
+    dt = q.dtype
+    if dt != torch.bfloat16 and dt != torch.uint8:
+        raise ValueError("q must be bf16 or uint8 (e4m3 codes)")
+    slots, ld = _pool(k_cache, "k_cache", dt)
+    B, cols = block_table.shape
+    H, d = q.shape[-2:]
+    if d != k_cache.shape[-1] or ld != d:
+        raise ValueError("q and k_cache must have dense rows of one length")
     if q.numel() != B * H * d or w.dtype != torch.float32 or w.numel() != B * H:
         raise ValueError("q must be [B, H, D] and w fp32 [B, H] with B = %d sequences" % B)
-    fp8 = q.dtype == torch.uint8
-    if fp8 and (q_scale is None or k_scale is None or q_scale.dtype != torch.float32 or
-                k_scale.dtype != torch.float32 or q_scale.numel() != B * H or
-                k_scale.numel() != slots):
-        raise ValueError("e4m3 keys need fp32 q_scale [B, H] and k_scale [slots]")
+    _contig(q, w)
+    fp8 = dt == torch.uint8
+    if fp8:
+        if q_scale is None or k_scale is None or q_scale.dtype != torch.float32 or \
+                k_scale.dtype != torch.float32 or q_scale.numel() != B * H or \
+                k_scale.numel() != slots:
+            raise ValueError("e4m3 keys need fp32 q_scale [B, H] and k_scale [slots]")
+        _contig(q_scale, k_scale)
     dev = _one_device(q, k_cache, w, block_table, seq_lens, scores, q_scale, k_scale)
     pg = make_paging(block_table, seq_lens, page_size, _pages(slots, page_size, "k_cache"))
-    with _On(dev, stream) as st:
-        most = block_table.shape[1] * page_size
-        if scores is None:
-            scores = torch.empty((B, most), dtype=torch.float32, device=dev)
-        if scores.dtype != torch.float32 or scores.dim() != 2 or scores.shape[0] != B or \
-                (scores.shape[1] > 1 and scores.stride(1) != 1):
-            raise ValueError("scores must be fp32 [%d, L] with contiguous rows" % B)
-        ld = scores.stride(0) if B > 1 else scores.shape[1]
-        _check(lib().ic_indexer_scores_paged(
-            _p(q), _p(q_scale) if fp8 else None, _p(k_cache), _p(k_scale) if fp8 else None, _p(w),
-            IC_E4M3 if fp8 else IC_BF16, B, H, d, ctypes.byref(pg), min(scores.shape[1], most),
-            _p(scores), ld, st))
+    most = cols * page_size
+    if scores is None:
+        scores = _new((B, most), torch.float32, dev, stream)
+    if scores.dtype != torch.float32 or scores.dim() != 2 or scores.shape[0] != B:
+        raise ValueError("scores must be fp32 [%d, L]" % B)
+    width = scores.shape[1]
+    ld = width
+    if not scores.is_contiguous():
+        if width > 1 and scores.stride(1) != 1:
+            raise ValueError("scores must have contiguous rows")
+        if B > 1:
+            ld = scores.stride(0)
+    _launch(dev, stream, lambda st: lib().ic_indexer_scores_paged(
+        q.data_ptr(), q_scale.data_ptr() if fp8 else None, k_cache.data_ptr(),
+        k_scale.data_ptr() if fp8 else None, w.data_ptr(), IC_E4M3 if fp8 else IC_BF16, B, H, d,
+        ctypes.byref(pg), width if width < most else most, scores.data_ptr(), ld, st))
     return scores
 
 
@@ -693,32 +760,26 @@ def ic_sparse_attn_paged(q, kv_cache, idx, block_table, seq_lens, scale: float, 
     [B, R, k] int32 token numbers of each query's own sequence (entries outside it are
     skipped), kv_cache [slots, w] or [pages, page_size, w] of kv_dtype (IC_BF16; uint8 rows:
     IC_E4M3 or IC_MXF4).  workspace: ic_attn_workspace_size bytes let few queries be split."""
-    _contig(q, idx, out, lse)
-    if q.dtype != torch.bfloat16 or q.dim() != 4 or idx.dtype != torch.int32 or \
-            idx.dim() != 3 or idx.shape[:2] != q.shape[:2] or q.shape[0] != block_table.shape[0]:
-        raise ValueError("q must be bf16 [B, R, H, D] and idx int32 [B, R, k], B = %d sequences" %
-                         block_table.shape[0])
-    if kv_dtype is None:
-        kv_dtype = IC_BF16 if kv_cache.dtype == torch.bfloat16 else None
-    if kv_dtype not in (IC_BF16, IC_E4M3, IC_MXF4):
-        raise ValueError("kv_dtype must be IC_BF16, IC_E4M3 or IC_MXF4")
-    slots, ld, _ = _pool(kv_cache, "kv_cache",
-                         (torch.bfloat16 if kv_dtype == IC_BF16 else torch.uint8,),
-                         _KV_ROW[kv_dtype])
+    if q.dtype != torch.bfloat16 or q.dim() != 4 or idx.dtype != torch.int32 or idx.dim() != 3:
+        raise ValueError("q must be bf16 [B, R, H, D] and idx int32 [B, R, k]")
     B, R, H, dk = q.shape
+    if idx.shape[0] != B or idx.shape[1] != R or block_table.shape[0] != B:
+        raise ValueError("q, idx and block_table must have one batch and one number of rows")
+    _contig(q, idx, out, lse)
+    kv_dtype, slots, ld = _kv_pool(kv_cache, kv_dtype)
     dev = _one_device(q, kv_cache, idx, block_table, seq_lens, out, lse, workspace)
     pg = make_paging(block_table, seq_lens, page_size, _pages(slots, page_size, "kv_cache"))
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty((B, R, H, 512), dtype=torch.bfloat16, device=dev)
-        if out.dtype != torch.bfloat16 or tuple(out.shape) != (B, R, H, 512):
-            raise ValueError("out must be bf16 %s" % ((B, R, H, 512),))
-        if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, R, H)):
-            raise ValueError("lse must be fp32 %s" % ((B, R, H),))
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().ic_sparse_attn_paged(
-            _p(q), _p(kv_cache), ld, ctypes.byref(pg), _p(idx), kv_dtype, B, R, H, dk, 512,
-            idx.shape[-1], float(scale), _p(out), _p(lse), _p(workspace), ws_bytes, st))
+    if out is None:
+        out = _new((B, R, H, 512), torch.bfloat16, dev, stream)
+    elif out.dtype != torch.bfloat16 or out.shape != (B, R, H, 512):
+        raise ValueError("out must be bf16 %s" % ((B, R, H, 512),))
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, R, H)):
+        raise ValueError("lse must be fp32 %s" % ((B, R, H),))
+    ws, ws_bytes = (None, 0) if workspace is None else (
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _launch(dev, stream, lambda st: lib().ic_sparse_attn_paged(
+        q.data_ptr(), kv_cache.data_ptr(), ld, ctypes.byref(pg), idx.data_ptr(), kv_dtype, B, R, H,
+        dk, 512, idx.shape[2], scale, out.data_ptr(), _ptr(lse), ws, ws_bytes, st))
     return out
 
 
