@@ -147,7 +147,10 @@ struct IdxCfg {
   static constexpr int OFF_CHIST = OFF_CBUF + CB * 8;
   static constexpr int OFF_CX = OFF_CHIST + (FUSED ? 256 * 4 : 0);
   static constexpr int OFF_MISC = OFF_CX + (FUSED ? FUSED_XINTS * 4 : 0);
-  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;  // + alignment slack
+  // pages: the pool rows of two runs of 32 pages (one-token instances)
+  static constexpr int OFF_PAGES = OFF_MISC + 32;
+  static constexpr int PAGE_BYTES = (TPM == 1 && !FUSED) ? 256 : 0;
+  static constexpr int SMEM_BYTES = OFF_PAGES + PAGE_BYTES + 1024;  // + alignment slack
   static_assert(!FUSED || (TPM == 1 && NSTG % NSETS == 0 && SETW == 4),
                 "the fused top-k runs in the one-token instance");
   static_assert(A_BYTES % 1024 == 0 && Q_BYTES % 1024 == 0, "swizzle atoms need 1 KB alignment");
@@ -531,77 +534,125 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
     if (warp == 0) {
       // ------------------------------------------------------------ TMA producer
       if constexpr (MODE == kIdxPaged) {
-        // The whole warp walks the tiles: lane l holds the numbers of pages base + l
-        // and base + 32 + l of the sequence (the second set is fetched 32 pages
-        // ahead, so no tile waits for the page table), lane 0 issues the copies, one
-        // per page or per 128 rows.  Rows past the sequence's end are not copied.
-        // A page number outside the pool reads as zeros (out of the map's bounds).
+        // Tiles go out in runs that lie within 32 aligned pages of a sequence: lane 0
+        // issues a run's tiles, a copy per page (or per 128 rows of a larger one), with
+        // the page numbers from shared memory, while the warp's loads of the next run's
+        // 32 numbers are in flight.  (Fetched one tile ahead instead, the page table's
+        // latency set the pace: 0.449 ms on 64 x 200K e4m3 keys in pages of 64; fetched
+        // and shuffled by the whole warp per tile: 0.402 ms.)  Rows past the sequence's
+        // end are not copied.  A page number outside the pool reads as zeros (out of the
+        // map's bounds).
+        const int shift = a.pg.shift, ps = 1 << shift;
+        const int per = ps < C::BM ? C::BM >> shift : 1;  // copies of a whole tile
+        const int rows = ps < C::BM ? ps : C::BM;         // rows of each
+        const int oob = a.pg.num_pages << shift;
+        int* pages = reinterpret_cast<int*>(smem + C::OFF_PAGES);  // [2][32]
         WorkIt<TPM, MODE> it{start[0], start[1], qb_tiles<TPM, MODE>(a, start[0])};
-        const int ps = 1 << a.pg.shift;
-        const int per = ps < C::BM ? C::BM >> a.pg.shift : 1;  // copies of a whole tile
-        const int rows = ps < C::BM ? ps : C::BM;              // rows of each
-        const int oob = a.pg.num_pages << a.pg.shift;
-        int stage = 0, cur_qb = -1, qloads = 0, base = 0, len = 0;
-        int cur = 0, nxt = 0;
+        int len = qb_info<TPM, MODE>(a, it.qb).Lk;
+        auto fetch = [&](int qb, int kt, int n) -> int {
+          const long p = ((static_cast<long>(kt) * C::BM >> shift) & ~31L) + lane;
+          int row = oob;
+          if ((p << shift) < n) {
+            const int e = a.pg.table[qb * a.pg.ld_table + p];
+            if (in_bounds(e >= 0 && e < a.pg.num_pages, kErrBoundsPage) && e >= 0 &&
+                e < a.pg.num_pages)
+              row = e << shift;
+          }
+          return row;
+        };
+        pages[lane] = fetch(it.qb, it.kt, len);
+        __syncwarp();
+        int stage = 0, cur_qb = -1, qloads = 0, half = 0;
         uint32_t ph = 0;
         long issued = 0;
-        auto fetch = [&](int qb, int p) -> int {
-          const int e = (static_cast<long>(p) << a.pg.shift) < len ? a.pg.table[qb * a.pg.ld_table + p] : -1;
-          return e >= 0 && e < a.pg.num_pages ? e : -1;
-        };
-        for (long i = 0; i < nitems; ++i) {
-          const int p0 = (it.kt * C::BM) >> a.pg.shift;
-          if (it.qb != cur_qb) {
-            len = qb_info<TPM, MODE>(a, it.qb).Lk;
-            base = p0 & ~31;
-            cur = fetch(it.qb, base + lane);
-            nxt = fetch(it.qb, base + 32 + lane);
-            if (!__all_sync(0xffffffffu, qloads == 0 || mbar_wait(qempty_bar, (qloads - 1) & 1,
-                                                                  abort_flag, kErrTimeoutProducer)))
-              break;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(qfull_bar, C::Q_BYTES);
-#pragma unroll
-              for (int kb = 0; kb < C::KBLK; ++kb)
-                tma_load_2d(q_base + kb * (C::N * 128), &tmQ, kb * C::ELEMS_128B, it.qb * 64,
-                            qfull_bar);
-            }
-            ++qloads;
-            cur_qb = it.qb;
-          } else if (p0 >= base + 32) {
-            base += 32;
-            cur = nxt;
-            nxt = fetch(it.qb, base + 32 + lane);
+        bool ok = true;
+        while (issued < nitems && ok) {
+          // the run's end, and where the next one begins
+          const long stop = (((static_cast<long>(it.kt) * C::BM >> shift) | 31L) + 1 << shift) /
+                            C::BM;
+          long m = (stop < it.nt ? stop : it.nt) - it.kt;
+          if (m > nitems - issued) m = nitems - issued;
+          WorkIt<TPM, MODE> nx = it;
+          nx.kt += static_cast<int>(m) - 1;
+          nx.advance(a);
+          int nlen = len, nrow = oob;
+          if (issued + m < nitems) {
+            if (nx.qb != it.qb) nlen = qb_info<TPM, MODE>(a, nx.qb).Lk;
+            nrow = fetch(nx.qb, nx.kt, nlen);
           }
-          if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), ph ^ 1, abort_flag,
-                                                 kErrTimeoutProducer)))
-            break;
-          const int left = len - it.kt * C::BM;
-          const int n = left >= C::BM ? per : (left + rows - 1) / rows;  // copies of this tile
-          if (lane == 0) mbar_arrive_expect_tx(full_bar(stage), n * rows * C::ROWB);
+          if (lane == 0) {
+            const int* pg = pages + 32 * half;
+            if (it.qb != cur_qb) {
+              ok = qloads == 0 ||
+                   mbar_wait(qempty_bar, (qloads - 1) & 1, abort_flag, kErrTimeoutProducer);
+              if (ok) {
+                mbar_arrive_expect_tx(qfull_bar, C::Q_BYTES);
+#pragma unroll
+                for (int kb = 0; kb < C::KBLK; ++kb)
+                  tma_load_2d(q_base + kb * (C::N * 128), &tmQ, kb * C::ELEMS_128B, it.qb * 64,
+                              qfull_bar);
+                ++qloads;
+                cur_qb = it.qb;
+              }
+            }
+            for (int t = 0; ok && t < m; ++t) {
+              const int s0 = (it.kt + t) * C::BM, in_page = s0 & (ps - 1);
+              const int left = len - s0;
+              const int n = left >= C::BM ? per : (left + rows - 1) / rows;  // its copies
+              const int* p = pg + ((s0 >> shift) & 31);
+              if (!mbar_wait(empty_bar(stage), ph ^ 1, abort_flag, kErrTimeoutProducer)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(full_bar(stage), n * rows * C::ROWB);
+              const uint32_t dst = a_base + stage * C::A_BYTES, fb = full_bar(stage);
+              auto copy = [&](int j, int krow) {
+#pragma unroll
+                for (int kb = 0; kb < C::KBLK; ++kb)
+                  tma_load_2d(dst + kb * (C::BM * 128) + j * rows * 128, &tmK,
+                              kb * C::ELEMS_128B, krow, fb);
+              };
+              // a whole tile's copies go out back to back (in a loop over n, each further
+              // copy costs 160 cycles instead of 45; predicated, each absent one 40)
+              auto four = [&](int j) {
+                const int4 r = *reinterpret_cast<const int4*>(p + j);
+                copy(j, r.x);
+                copy(j + 1, r.y);
+                copy(j + 2, r.z);
+                copy(j + 3, r.w);
+              };
+              if (n == 1) {
+                copy(0, p[0] + in_page);
+              } else if (n == 2) {
+                const int2 r = *reinterpret_cast<const int2*>(p);
+                copy(0, r.x);
+                copy(1, r.y);
+              } else if (n == 4) {
+                four(0);
+              } else if (n == 8) {
+                four(0);
+                four(4);
+              } else {
+                for (int j = 0; j < n; ++j) copy(j, p[j]);
+              }
+              ++issued;
+              if (++stage == C::STAGES) {
+                stage = 0;
+                ph ^= 1;
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          issued = __shfl_sync(0xffffffffu, issued, 0);
+          half ^= 1;
+          pages[32 * half + lane] = nrow;
           __syncwarp();
-          for (int j = 0; j < n; ++j) {
-            const int page = __shfl_sync(0xffffffffu, cur, (p0 + j) & 31);
-            const bool ok = in_bounds(page >= 0, kErrBoundsPage) && page >= 0;
-            const int krow =
-                ok ? (page << a.pg.shift) + ((it.kt * C::BM) & (ps - 1)) : oob;
-            if (lane == 0) {
-#pragma unroll
-              for (int kb = 0; kb < C::KBLK; ++kb)
-                tma_load_2d(a_base + stage * C::A_BYTES + kb * (C::BM * 128) + j * rows * 128,
-                            &tmK, kb * C::ELEMS_128B, krow, full_bar(stage));
-            }
-          }
-          ++issued;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            ph ^= 1;
-          }
-          it.advance(a);
+          it = nx;
+          len = nlen;
         }
         if (*abort_flag && lane == 0) {
           // let every copy started land before the CTA's smem goes away
-          long n = issued < C::STAGES ? issued : C::STAGES;
+          const long n = issued < C::STAGES ? issued : C::STAGES;
           for (long j = issued - n; j < issued; ++j)
             mbar_wait_drain(full_bar(static_cast<int>(j % C::STAGES)),
                             static_cast<uint32_t>((j / C::STAGES) & 1));
@@ -725,6 +776,7 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
       uint32_t aph = 0;
       int cur_qb = -1;
       QbInfo pq{};  // paged: the sequence's, read once per sequence
+      int pnext = -1, pnext_qb = -1;  // paged: this lane's page of the set's next tile
       // head weights of this warp's tokens: the warp's shared copy (wsl), written
       // when a query block starts; a warp with several tokens keeps them in registers
       // (wr), a one-token warp reads them with one broadcast load per 4 heads
@@ -777,13 +829,18 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
         const bool key_ok = s < qi.Lk;
         float ks = 1.f;
         if constexpr (FP8 && MODE == kIdxPaged) {
-          if (key_ok) {
-            const int page = __ldg(a.pg.table + it.qb * a.pg.ld_table + (s >> a.pg.shift));
-            ks = 0.f;
-            if (page >= 0 && page < a.pg.num_pages)
-              ks = a.k_scale[(static_cast<long>(page) << a.pg.shift) +
-                             (s & ((1 << a.pg.shift) - 1))];
-          }
+          // the page number was fetched while this set's previous tile was reduced,
+          // unless the sequence began since
+          const int* row = a.pg.table + it.qb * a.pg.ld_table;
+          int page = pnext;
+          if (it.qb != pnext_qb) page = key_ok ? __ldg(row + (s >> a.pg.shift)) : -1;
+          ks = 0.f;
+          if (page >= 0 && page < a.pg.num_pages)
+            ks = a.k_scale[(static_cast<long>(page) << a.pg.shift) +
+                           (s & ((1 << a.pg.shift) - 1))];
+          const int sn = s + C::NSETS * C::BM;
+          pnext = sn < qi.Lk ? __ldg(row + (sn >> a.pg.shift)) : -1;
+          pnext_qb = it.qb;
         } else if constexpr (FP8) {
           ks = key_ok ? a.k_scale[qi.krow0 + s] : 0.f;
         }
