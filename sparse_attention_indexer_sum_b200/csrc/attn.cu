@@ -207,54 +207,6 @@ __device__ __forceinline__ long attn_page_row(const PagedArgs& pg, long b, int s
   return (static_cast<long>(page) << pg.shift) + (s & ((1 << pg.shift) - 1));
 }
 
-// The same for the 4-bit rows (400 bytes at slot offset 768: 512 e2m1 codes, two a
-// byte with the even dim low, 16 e8m0 block scales, 64 bf16 rope dims).  Lane l owns
-// latent dims 16l..16l+15, half of block l / 2.  A code times a power of two is exact
-// in bf16.  Rows without a copy become zeros.
-__device__ __forceinline__ void attn_dequant_rows4(uint8_t* stage_rows, unsigned valid, int pw) {
-  const int lane = threadIdx.x & 31;
-  uint8_t* rows = stage_rows + 8 * pw * AT_ROWB;
-  const unsigned mine = (valid >> (8 * pw)) & 0xFFu;
-  uint2 codes[8];
-  uint4 rope[8];
-  unsigned sc[8];
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const uint8_t* raw = rows + r * AT_ROWB + (AT_ROWB - KV4_ROW_BYTES);
-    codes[r] = *reinterpret_cast<const uint2*>(raw + 8 * lane);
-    sc[r] = raw[256 + (lane >> 1)];
-    rope[r] = lane < 8 ? *reinterpret_cast<const uint4*>(raw + 272 + 16 * lane)
-                       : make_uint4(0, 0, 0, 0);
-  }
-  __syncwarp();
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    uint8_t* row = rows + r * AT_ROWB;
-    uint32_t o[8];
-    if ((mine >> r) & 1u) {
-      const float s = e8m0_value(sc[r]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w = i < 4 ? codes[r].x : codes[r].y;
-        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(
-            static_cast<__nv_fp4x2_storage_t>((w >> (8 * (i & 3))) & 0xFFu), __NV_E2M1);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        __nv_bfloat162 v = __floats2bfloat162_rn(f.x * s, f.y * s);
-        o[i] = *reinterpret_cast<uint32_t*>(&v);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = 0u;
-      rope[r] = make_uint4(0, 0, 0, 0);
-    }
-    *reinterpret_cast<uint4*>(row + 32 * lane) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(row + 32 * lane + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-    if (lane < 8) *reinterpret_cast<uint4*>(row + 1024 + 16 * lane) = rope[r];
-  }
-  fence_proxy_async_smem();  // before the next copies land where these stores went
-  __syncwarp();
-}
-
 // CTA holding (query, tile) pair t of the split list: the largest c with
 // floor(c * tot / G) <= t.
 __host__ __device__ __forceinline__ long attn_cta_of(long t, long tot, long G) {
@@ -307,7 +259,8 @@ __device__ __forceinline__ long attn_nitems(const AttnArgs& a) {
   const long lo = a.tot * blockIdx.x / gridDim.x, hi = a.tot * (blockIdx.x + 1) / gridDim.x;
   return hi > lo ? (hi - 1) / a.tq - lo / a.tq + 1 : 0;
 }
-// Item j of this CTA.
+// Item j of this CTA (tiles of BK keys).
+template <int BK = AT_BK>
 __device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, long j) {
   AttnItem x;
   if (!a.split) {
@@ -322,8 +275,8 @@ __device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, long j) {
   const long q0 = x.qrow * a.tq;
   const long t0 = lo > q0 ? lo : q0;
   const long t1 = hi < q0 + a.tq ? hi : q0 + a.tq;
-  x.beg = static_cast<int>((t0 - q0) * AT_BK);
-  x.end = min(static_cast<int>((t1 - q0) * AT_BK), a.k);
+  x.beg = static_cast<int>((t0 - q0) * BK);
+  x.end = min(static_cast<int>((t1 - q0) * BK), a.k);
   if (x.end < x.beg) x.end = x.beg;
   x.pslot = x.qrow * a.maxp + (blockIdx.x - attn_cta_of(q0, a.tot, gridDim.x));
   return x;
@@ -361,7 +314,7 @@ template <int FMT, int ADDR>
 __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
                                               const AttnAddrParam<ADDR>& sg) {
   constexpr bool RAW = FMT != kFmtBf16;  // rows that the producers expand to bf16
-  constexpr int RAW_BYTES = FMT == kFmtMxf4 ? KV4_ROW_BYTES : KV8_ROW_BYTES;
+  constexpr int RAW_BYTES = KV8_ROW_BYTES;
   const int lane = threadIdx.x & 31;
   const int pw = (threadIdx.x - AT_CONSUMERS) >> 5;
   volatile int* abort = &sm.abort;
@@ -387,10 +340,7 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.rawf[pend_stage]), pend_ph, abort,
                                            kErrTimeoutProducer)))
       return false;
-    if constexpr (FMT == kFmtMxf4)
-      attn_dequant_rows4(&sm.kv[pend_stage][0][0], pend_valid, pw);
-    else
-      attn_dequant_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
+    attn_dequant_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
     if constexpr (FMT == kFmtE4m3 && ADDR == kAddrPaged)
       attn_zero_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
     __syncwarp();
@@ -855,6 +805,9 @@ __global__ void attn_combine_kernel(const float* part_o, const float* part_ml, i
   o[1] = pack_bf16((a0.z + a1.z) * il, (a0.w + a1.w) * il);
 }
 
+// the kernel of the 4-bit rows (its launch function is used below)
+#include "attn_kv4.cuh"
+
 // Split plan for few queries: G CTAs over the items*tq (query, tile) pairs, each
 // query cut into at most 64 pieces (G <= 63 * items keeps a range >= tq / 63 tiles).
 struct SplitPlan {
@@ -862,11 +815,11 @@ struct SplitPlan {
   int G, tq, maxp;
   long tot;
 };
-static SplitPlan split_plan(long items, int k) {
+static SplitPlan split_plan(long items, int k, int bk = AT_BK) {
   SplitPlan p{false, 0, 0, 0, 0};
   const long nsm = num_sms();
   if (items <= 0 || items >= 4 * nsm) return p;  // enough queries for every SM
-  p.tq = (k + AT_BK - 1) / AT_BK;
+  p.tq = (k + bk - 1) / bk;
   p.tot = items * p.tq;
   long G = nsm;
   if (G > p.tot) G = p.tot;
@@ -884,9 +837,11 @@ static SplitPlan split_plan(long items, int k) {
 
 size_t attn_mla_ws_bytes(int batch, int rows, int k) {
   const long items = static_cast<long>(batch) * rows;
-  const SplitPlan p = split_plan(items, k);
-  if (!p.split) return 0;
-  return static_cast<size_t>(items) * p.maxp * AT_H * (AT_DV + 2) * sizeof(float);
+  // of either tile size (the 4-bit rows' kernel has tiles of K4_BK keys)
+  const SplitPlan p = split_plan(items, k), p4 = split_plan(items, k, K4_BK);
+  if (!p.split && !p4.split) return 0;
+  const int maxp = p.maxp > p4.maxp ? p.maxp : p4.maxp;
+  return static_cast<size_t>(items) * maxp * AT_H * (AT_DV + 2) * sizeof(float);
 }
 
 template <int FMT, int ADDR>
@@ -910,7 +865,7 @@ ic_status launch_attn_mla(const void* q, const void* kv, long ld_kv, const int* 
   if (nseg < 0 || nseg > IC_MAXSEG || (nseg > 0 && (batch != 1 || !segs)))
     return fail(IC_ERR_INVALID_ARG, "attn: bad segment list (%d)", nseg);
   if (items == 0) return IC_OK;
-  SplitPlan p = split_plan(items, k);
+  SplitPlan p = split_plan(items, k, fmt == kFmtMxf4 ? K4_BK : AT_BK);
   const size_t need = static_cast<size_t>(items) * p.maxp * AT_H * (AT_DV + 2) * sizeof(float);
   // no room, or a workspace the merge's 16-byte loads cannot use: one CTA per query
   if (p.split && (ws == nullptr || need > ws_bytes || reinterpret_cast<uintptr_t>(ws) % 16 != 0))
@@ -938,7 +893,7 @@ ic_status launch_attn_mla(const void* q, const void* kv, long ld_kv, const int* 
   const long grid = p.split ? p.G : (items < num_sms() ? items : num_sms());
   ic_status st;
   if (pages) {
-    st = fmt == kFmtMxf4   ? launch_attn_inst<kFmtMxf4, kAddrPaged>(a, *pages, grid, stream)
+    st = fmt == kFmtMxf4   ? launch_attn_kv4(a, *pages, grid, stream)
          : fmt == kFmtE4m3 ? launch_attn_inst<kFmtE4m3, kAddrPaged>(a, *pages, grid, stream)
                            : launch_attn_inst<kFmtBf16, kAddrPaged>(a, *pages, grid, stream);
   } else if (nseg > 0) {
