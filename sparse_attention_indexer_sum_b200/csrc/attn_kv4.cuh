@@ -3,37 +3,63 @@
 //
 // A row is 400 bytes: 512 e2m1 codes, 16 e8m0 scales (one per 32 dims), 64 bf16 rope
 // dims.  Gathering it moves a third of a bf16 row's bytes, so what bounds this kernel is
-// no longer the gather but turning codes into operands of the warp-level MMA:
-//   * the raw rows stay as they are in shared memory (tiles of K4_BK keys, K4_STAGES
-//     deep); no bf16 copy of a tile exists.  Each code is expanded twice, in the
-//     registers that feed QK and in those that feed PV;
-//   * QK: the contraction's order of dims is free, so lane c of a quad takes 32
-//     consecutive dims -- one block, one scale -- of its key with one 16-byte load, and
-//     Q's fragments are loaded in the same order;
-//   * PV: a lane takes 8 consecutive dims of two keys with two 4-byte loads, and the
-//     order of output dims that follows gives every lane 16 consecutive ones to store.
-// Expansion: byte permutes (prmt) look up four codes at a time in a table of the eight
-// magnitudes, high and low bytes of bf16 apart; QK's table is scaled beforehand, PV's
-// values after.  A code times a power of two is exact in bf16.
-// Rows without an entry are filled with zeros by their copies.
+// no longer the gather but turning codes into operands of the warp-level MMA and moving
+// those through shared memory:
+//   * producer warps copy the raw rows with 16-byte cp.async (a row needs 25, which a
+//     warp issues for several rows at once); rows without an entry become zeros;
+//   * the eight consumer warps expand every code once, in the registers that feed QK:
+//     warp (half, group) covers dims 256 half..+256 of keys 8 group..+8.  The
+//     contraction's order of dims is free, so a lane takes 64 consecutive dims -- two
+//     blocks, two scales -- of its key with two 16-byte loads, and Q's fragments are
+//     loaded in the same order.  The expanded dims also go to a bf16 tile, swizzled so
+//     that neither these stores nor PV's transposed loads meet bank conflicts;
+//   * PV reads that tile; the order of the eight dims in each of its 16-byte pieces is
+//     the one the expansion leaves, undone when O is stored.
+// Expansion: a code s e e m, its sign at bit 15 and e e m at bits 8..6, is the bf16
+// number value * 2^-126 (0.5 becomes a subnormal); one AND, one multiplication (both
+// shifts at once) and one AND move two codes, and a bf16 multiplication by 2^(E - 1)
+// gives two exact scaled values.  That is half integer-pipe work of a byte-permute table
+// (which with a second expansion for PV instead of the bf16 tile measured 561 us on
+// 3 x 341 queries of 2048 rows, its integer pipe the limit at 2300 cycles per 32 keys).
 
-constexpr int K4_BK = 64;                       // keys per tile
-constexpr int K4_STAGES = 4;
-constexpr int K4_PROD_WARPS = 4;                // each copies 16 of a tile's 64 rows
+constexpr int K4_BK = 32;                       // keys per tile
+constexpr int K4_STAGES = 6;                    // even: a stage always serves one group
+constexpr int K4_GROUPS = 2;
+constexpr int K4_GTHREADS = AT_CONSUMERS / K4_GROUPS;
+constexpr int K4_PROD_WARPS = 4;
+constexpr int K4_PROD_ROWS = K4_BK / K4_PROD_WARPS;  // rows of a tile that each copies
 constexpr int K4_THREADS = AT_CONSUMERS + 32 * K4_PROD_WARPS;
+// Registers per thread after the roles part: the block starts with 168 each (64512 in
+// all), the producers give up theirs above K4_PREGS and the consumers take K4_CREGS.
+constexpr int K4_CREGS = 216, K4_PREGS = 72;
+static_assert(AT_CONSUMERS * K4_CREGS + 32 * K4_PROD_WARPS * K4_PREGS <= 168 * K4_THREADS,
+              "the split must not exceed what the block was launched with");
+static_assert(AT_CONSUMERS % 128 == 0 && K4_PROD_WARPS == 4, "whole warpgroups change registers");
 constexpr int K4_CHUNKS = KV4_ROW_BYTES / 16;   // 16-byte copies per row
-constexpr int K4_SROW = 72;                     // padded partial-score row (floats)
-constexpr int K4_PROW = 72;                     // padded P row (bf16)
+constexpr int K4_SROW = K4_BK + 8;              // padded partial-score row (floats)
+constexpr int K4_PROW = K4_BK + 8;              // padded P row (bf16)
+constexpr int K4_RROW = 144;                    // padded rope row (bytes)
+static_assert(K4_STAGES % K4_GROUPS == 0 && K4_CHUNKS <= 32, "stages per group, lanes per row");
 
-struct Kv4Smem {
-  alignas(128) uint8_t raw[K4_STAGES][K4_BK][KV4_ROW_BYTES];
-  alignas(128) uint8_t q[AT_H][AT_ROWB];
-  alignas(16) float s_part[4][AT_H][K4_SROW];
+struct Kv4Stage {
+  uint8_t codes[K4_BK][256];  // 16-byte piece i of row r at place i ^ (r & 1)
+  uint8_t rope[K4_BK][K4_RROW];
+  uint8_t scale[K4_BK][16];
+};
+struct Kv4Group {  // one consumer group's own
+  alignas(128) uint8_t v[K4_BK][1024];  // its expanded tile (kv4_vplace); at an item's end its O
+  alignas(16) float s_part[2][AT_H][K4_SROW];
   alignas(16) __nv_bfloat16 p[AT_H][K4_PROW];
   float alpha[AT_H];
   float fin_m[AT_H], fin_l[AT_H];
+};
+static_assert(sizeof(Kv4Group::v) == AT_H * AT_DV * sizeof(float), "O of an item fits the tile");
+struct Kv4Smem {
+  alignas(128) Kv4Stage raw[K4_STAGES];
+  Kv4Group grp[K4_GROUPS];
+  alignas(128) uint8_t q[AT_H][AT_ROWB];
   alignas(16) int ibuf[2][AT_MAXK];
-  alignas(8) uint16_t vmask[K4_STAGES][4];      // bit j of [w]: row 16w + j has an entry
+  alignas(4) uint8_t vmask[K4_STAGES][K4_PROD_WARPS];  // bit j of [w]: row 8w + j has an entry
   int last[K4_STAGES];
   alignas(8) uint64_t full[K4_STAGES];
   uint64_t empty[K4_STAGES];
@@ -55,15 +81,29 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Producers walk the items as attn_producer's do; warp pw copies rows 16pw..16pw+15 of
-// every tile, 25 16-byte copies each, spread over its lanes.
+// Producers walk the items as attn_producer's do; warp pw copies rows 8pw..8pw+7 of
+// every tile, lane l < 25 the row's 16-byte piece l.
 __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, const PagedArgs& pg) {
   const int lane = threadIdx.x & 31;
   const int pw = (threadIdx.x - AT_CONSUMERS) >> 5;
   volatile int* abort = &sm.abort;
   const bool bulk = a.idx_bulk != 0;
-  const uint8_t* kv = reinterpret_cast<const uint8_t*>(a.kv);
-  const uint32_t raw0 = smem_u32(&sm.raw[0][0][0]);
+  // this lane's piece: where it lies in a stage for even and odd rows, and the row step
+  uint32_t at0, at1, step;
+  if (lane < 16) {
+    at0 = offsetof(Kv4Stage, codes) + 16 * lane;
+    at1 = offsetof(Kv4Stage, codes) + 16 * (lane ^ 1);
+    step = 256;
+  } else if (lane == 16) {
+    at0 = at1 = offsetof(Kv4Stage, scale);
+    step = 16;
+  } else {
+    at0 = at1 = offsetof(Kv4Stage, rope) + 16 * (lane - 17);
+    step = K4_RROW;
+  }
+  at0 += smem_u32(&sm.raw[0]) + K4_PROD_ROWS * pw * step;
+  at1 += smem_u32(&sm.raw[0]) + K4_PROD_ROWS * pw * step;
+  const uint8_t* src0 = reinterpret_cast<const uint8_t*>(a.kv) + 16 * lane;
   int stage = 0, ib = 0, qloads = 0;
   uint32_t ph = 0, iph[2] = {0u, 0u};
   int ipending[2] = {0, 0};
@@ -120,41 +160,43 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
                  smem_u32(&sm.qfull));
       ++qloads;
     }
-    // the pool row of row (16pw + lane mod 16) of tile t, read one tile ahead
-    auto pool_row = [&](int t) -> long {
-      const int j = t * K4_BK + 16 * pw + (lane & 15);
+    // the pool row of row (8pw + lane mod 8) of tile t, read one tile ahead
+    auto pool_row = [&](int t) -> int {
+      const int j = t * K4_BK + K4_PROD_ROWS * pw + (lane & (K4_PROD_ROWS - 1));
       const int s = (t < ntiles && j < cnt) ? ilist[j] : -1;
       if (!in_bounds(s >= -1 && s < len, kErrBoundsGather) || s < 0 || s >= len) return -1;
-      return attn_page_row(pg, b, s);
+      return static_cast<int>(attn_page_row(pg, b, s));
     };
-    const int nt = ntiles > 0 ? ntiles : 1;  // an empty item still ends with one (empty) tile
-    long prow = pool_row(0);
+    // the groups take turns: an even number of tiles, at least two
+    const int nt = ntiles > 2 ? (ntiles + 1) & ~1 : 2;
+    int prow = pool_row(0), pnext = pool_row(1);
     bool ok = true;
     for (int t = 0; t < nt; ++t) {
-      const long pnext = pool_row(t + 1);
+      const int pnext2 = pool_row(t + 2);
       if (!mbar_wait(smem_u32(&sm.empty[stage]), ph ^ 1, abort, kErrTimeoutProducer)) {
         ok = false;
         break;
       }
-      const unsigned valid = __ballot_sync(0xffffffffu, prow >= 0) & 0xFFFFu;
-      const uint32_t dst = raw0 + (stage * K4_BK + 16 * pw) * KV4_ROW_BYTES;
+      const unsigned valid = __ballot_sync(0xffffffffu, prow >= 0) & ((1u << K4_PROD_ROWS) - 1u);
+      const uint32_t so = stage * static_cast<uint32_t>(sizeof(Kv4Stage));
+      if (t < ntiles) {  // a tile without entries is not looked at
 #pragma unroll
-      for (int i = 0; i < (16 * K4_CHUNKS + 31) / 32; ++i) {
-        const int c = lane + 32 * i;
-        const int r = c / K4_CHUNKS;  // row of the warp's 16
-        const long row = __shfl_sync(0xffffffffu, prow, r & 15);
-        if (c < 16 * K4_CHUNKS)
-          cp_async16(dst + 16 * c, kv + (row >= 0 ? row * a.ld_kv + 16 * (c - r * K4_CHUNKS) : 0),
-                     row >= 0);
+        for (int r = 0; r < K4_PROD_ROWS; ++r) {
+          const int row = __shfl_sync(0xffffffffu, prow, r);
+          if (lane < K4_CHUNKS)
+            cp_async16(((r & 1) ? at1 : at0) + so + r * step,
+                       src0 + (row >= 0 ? static_cast<long>(row) * a.ld_kv : 0), row >= 0);
+        }
       }
       const uint32_t fb = smem_u32(&sm.full[stage]);
       cp_async_arrive(fb);
       if (lane == 0) {
-        sm.vmask[stage][pw] = static_cast<uint16_t>(valid);
-        if (pw == 0) sm.last[stage] = (t == nt - 1);
+        sm.vmask[stage][pw] = static_cast<uint8_t>(valid);
+        if (pw == 0) sm.last[stage] = t >= nt - K4_GROUPS;
         mbar_arrive(fb);
       }
       prow = pnext;
+      pnext = pnext2;
       if (++stage == K4_STAGES) {
         stage = 0;
         ph ^= 1;
@@ -174,278 +216,293 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
 }
 
 // ---------------------------------------------------------------- codes to bf16
-// The eight e2m1 magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 as bf16: high bytes of the first
-// and last four, low bytes of the same.
-struct E2m1Table {
-  uint32_t h0, h1, l0, l1;
-};
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
                                    *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// The table times the power of two of e8m0 code e (0 counts as 0 instead of 2^-127, which
-// no result can show; 255: zeros become NaN, as a NaN block's codes are 0).
-__device__ __forceinline__ E2m1Table e2m1_table(uint32_t e) {
-  const uint32_t s = e * 0x00800080u;
-  const uint32_t a = bf16x2_mul(0x3F000000u, s), b = bf16x2_mul(0x3FC03F80u, s);
-  const uint32_t c = bf16x2_mul(0x40404000u, s), d = bf16x2_mul(0x40C04080u, s);
-  return E2m1Table{__byte_perm(a, b, 0x7531), __byte_perm(c, d, 0x7531),
-                   __byte_perm(a, b, 0x6420), __byte_perm(c, d, 0x6420)};
-}
-// The eight codes of w (code i in bits 4i..4i+3) as four bf16 pairs (0, 1), (2, 3), ...
-__device__ __forceinline__ void e2m1_expand(uint32_t w, const E2m1Table& t, uint32_t (&o)[4]) {
-  const uint32_t m = w & 0x77777777u, w4 = w << 4;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const uint32_t sel = half ? m >> 16 : m;
-    uint32_t hi = __byte_perm(t.h0, t.h1, sel);
-    const uint32_t lo = __byte_perm(t.l0, t.l1, sel);
-    // the codes' sign bits in the top bits of four bytes
-    hi |= __byte_perm(w, w4, half ? 0x3726 : 0x1504) & 0x80808080u;
-    o[2 * half] = __byte_perm(lo, hi, 0x5140);
-    o[2 * half + 1] = __byte_perm(lo, hi, 0x7362);
-  }
+// The eight codes of w (code i in bits 4i..4i+3), times the scale pair s (both halves
+// 2^(E - 1)), as the bf16 pairs (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ void e2m1_expand(uint32_t w, uint32_t s, uint32_t* o) {
+  const uint32_t w8 = w >> 8;
+  constexpr uint32_t kMask = 0x81C081C0u;  // bits 15 and 8..6 of each half
+  o[0] = bf16x2_mul(((w & 0x000F000Fu) * 0x1040u) & kMask, s);
+  o[1] = bf16x2_mul(((w & 0x00F000F0u) * 0x0104u) & kMask, s);
+  o[2] = bf16x2_mul(((w8 & 0x000F000Fu) * 0x1040u) & kMask, s);
+  o[3] = bf16x2_mul(((w8 & 0x00F000F0u) * 0x0104u) & kMask, s);
 }
 
-// Partial scores of this warp: Q over dims 128kq..+128 and rope dims 16kq..+16 against
-// keys 32kh..32kh+31 of the tile at raw.  c[j]: keys 32kh + 8j..+8.
-__device__ __forceinline__ void kv4_qk(const uint8_t* raw, const uint32_t (&qa)[9][4], int kq,
-                                       int kh, int lane, float (&c)[4][4]) {
-  const int g = lane >> 2, cq = lane & 3;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint8_t* row = raw + (32 * kh + 8 * j + g) * KV4_ROW_BYTES;
-    const uint4 w = *reinterpret_cast<const uint4*>(row + 64 * kq + 16 * cq);
-    const E2m1Table t = e2m1_table(row[256 + 4 * kq + cq]);
-    c[j][0] = c[j][1] = c[j][2] = c[j][3] = 0.f;
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t o[4];
-      e2m1_expand(ws[i], t, o);
-      mma_bf16(c[j], qa[2 * i], o[0], o[1]);
-      mma_bf16(c[j], qa[2 * i + 1], o[2], o[3]);
-    }
-  }
-  const uint32_t rope = smem_u32(raw) + (32 * kh + (lane & 7) + 8 * (lane >> 4)) * KV4_ROW_BYTES +
-                        272 + 32 * kq + 16 * ((lane >> 3) & 1);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t b0, b1, b2, b3;
-    ldsm_x4(rope + 16 * j * KV4_ROW_BYTES, b0, b1, b2, b3);
-    mma_bf16(c[2 * j], qa[8], b0, b1);
-    mma_bf16(c[2 * j + 1], qa[8], b2, b3);
-  }
+// Place (in 16-byte pieces) of piece L (0..63) of key r in its 1024-byte row of the
+// expanded tile.  The stores of a quad's lanes go to pieces 8 apart, of two keys at a
+// time; the transposed loads take one piece of eight consecutive keys.
+__device__ __forceinline__ int kv4_vplace(int L, int r) {
+  return L ^ ((L >> 3) & 3) ^ ((r & 1) << 2) ^ ((r >> 1) & 3);
 }
 
-// O = alpha O + P V over the tile at raw, for dims 64w..64w+63.  Output column n of MMA j
-// is dim 64w + 8n + j.
-__device__ __forceinline__ void kv4_pv(const uint8_t* raw, uint32_t pbase, float al0, float al1,
-                                       int warp, int lane, float (&o)[8][4]) {
-  const int g = lane >> 2, cq = lane & 3;
-  const E2m1Table t{0x3F3F3F00u, 0x40404040u, 0xC0800000u, 0xC0804000u};
+// Expands the codes of this warp's share of a tile into the bf16 tile at v (a shared
+// address) and multiplies them with Q: dims 256 half..+256 and rope dims 32 half..+32 of
+// keys 16 part..+16 (lane: keys g and g + 8 of them, two blocks of dims).
+__device__ __forceinline__ void kv4_qk(const Kv4Stage& raw, uint32_t v,
+                                       const uint32_t (&qa)[18][4], int half, int part, int lane,
+                                       float (&c)[2][4]) {
+  const int g = lane >> 2, cq = lane & 3, r = 16 * part + g;
+  const int blk = 8 * half + 2 * cq;
+  uint32_t e2[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    o[i][0] *= al0;
-    o[i][1] *= al0;
-    o[i][2] *= al1;
-    o[i][3] *= al1;
+  for (int n = 0; n < 2; ++n)
+    e2[n] = *reinterpret_cast<const uint16_t*>(&raw.scale[r + 8 * n][blk]);
+  // 2^(E - 1) as bf16 needs E <= 128: larger scales (and NaN) are finished below
+  const bool big = __any_sync(0xffffffffu, max(max(e2[0] & 0xFFu, e2[0] >> 8),
+                                               max(e2[1] & 0xFFu, e2[1] >> 8)) > 128u);
+  // the pieces 8m..8m+7 (m = 4 half + cq) of rows r and r + 8 have places 8m + (i ^ x)
+  const uint32_t vb = v + r * 1024 + 16 * kv4_vplace(4 * blk, r);
+  float d[2][4];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+    d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
   }
-  const int pr = (lane & 7) + 8 * ((lane >> 3) & 1);
 #pragma unroll
-  for (int ks = 0; ks < K4_BK / 16; ++ks) {
-    uint32_t pa[4];
-    ldsm_x4(pbase + (pr * K4_PROW + 16 * ks + 8 * (lane >> 4)) * 2, pa[0], pa[1], pa[2], pa[3]);
-    uint32_t v[2][8];  // [keys +0,1 / +8,9][dim]
+  for (int u = 0; u < 2; ++u) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const uint8_t* ra = raw + (16 * ks + 8 * hf + 2 * cq) * KV4_ROW_BYTES;
-      const uint8_t* rb = ra + KV4_ROW_BYTES;
-      const uint32_t wa = *reinterpret_cast<const uint32_t*>(ra + 32 * warp + 4 * g);
-      const uint32_t wb = *reinterpret_cast<const uint32_t*>(rb + 32 * warp + 4 * g);
-      const uint32_t ea = ra[256 + 2 * warp + (g >> 2)], eb = rb[256 + 2 * warp + (g >> 2)];
-      const uint32_t s = (ea << 7) | (eb << 23);
-      // codes of both keys side by side: dims 0, 2, 4, 6 and 1, 3, 5, 7
-      const uint32_t t0 = (wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u);
-      const uint32_t t1 = ((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u);
-      uint32_t e0[4], e1[4];
-      e2m1_expand(t0, t, e0);
-      e2m1_expand(t1, t, e1);
+    for (int n = 0; n < 2; ++n) {
+      const uint4 w =
+          *reinterpret_cast<const uint4*>(&raw.codes[r + 8 * n][16 * ((blk + u) ^ (r & 1))]);
+      const uint32_t e = (e2[n] >> (8 * u)) & 0xFFu;
+      const uint32_t s = ((e < 128u ? e : 128u) + 126u) * 0x00800080u;
+      uint32_t o[16];
+      e2m1_expand(w.x, s, o);
+      e2m1_expand(w.y, s, o + 4);
+      e2m1_expand(w.z, s, o + 8);
+      e2m1_expand(w.w, s, o + 12);
+      if (big) {  // the rest of larger scales: 2^(E - 128), or NaN
+        const uint32_t s2 =
+            e == 255u ? 0x7FFF7FFFu : ((e > 128u ? e - 128u : 0u) + 127u) * 0x00800080u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = bf16x2_mul(o[i], s2);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[hf][2 * i] = bf16x2_mul(e0[i], s);
-        v[hf][2 * i + 1] = bf16x2_mul(e1[i], s);
+        mma_bf16(c[n], qa[8 * u + 2 * i], o[4 * i], o[4 * i + 1]);
+        mma_bf16(d[n], qa[8 * u + 2 * i + 1], o[4 * i + 2], o[4 * i + 3]);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mma_bf16(o[j], pa, v[0][j], v[1][j]);
+      for (int i = 0; i < 4; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                         (vb ^ (16u * (4 * u + i))) + 8192u * n),
+                     "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                     : "memory");
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    uint32_t b0, b1, b2, b3;
+    ldsm_x4(smem_u32(&raw.rope[16 * part + 8 * n + (lane & 7)][64 * half + 16 * (lane >> 3)]), b0,
+            b1, b2, b3);
+    mma_bf16(c[n], qa[16], b0, b1);
+    mma_bf16(d[n], qa[17], b2, b3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[n][i] += d[n][i];
   }
 }
 
-__device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  volatile int* abort = &sm.abort;
-  const int kq = warp >> 1, kh = warp & 1;  // QK: dim quarter, key half of the tile
-  const int g = lane >> 2, cq = lane & 3;
-  const int sh = 2 * warp + (lane >> 4);    // softmax: head of this lane
-  const int sk = 4 * (lane & 15);           // and its four keys
-  int stage = 0;
-  uint32_t ph = 0;
-  int rel = -1;  // stage of the previous tile, released after the next partial barrier
-  const long nj = attn_nitems(a);
-  auto store_partial = [&](const float (&c)[4][4]) {
-    float* sp = &sm.s_part[kq][0][0] + 32 * kh + 2 * cq;
+// O = alpha O + P V over the expanded tile at v, for dims 128w..128w+127.
+__device__ __forceinline__ void kv4_pv(uint32_t v, uint32_t pbase, float al0, float al1, int w,
+                                       int lane, float (&o)[16][4]) {
+  // most tiles do not raise any maximum
+  if (!__all_sync(0xffffffffu, al0 == 1.f && al1 == 1.f)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<float2*>(sp + g * K4_SROW + 8 * j) = make_float2(c[j][0], c[j][1]);
-      *reinterpret_cast<float2*>(sp + (g + 8) * K4_SROW + 8 * j) = make_float2(c[j][2], c[j][3]);
+    for (int i = 0; i < 16; ++i) {
+      o[i][0] *= al0;
+      o[i][1] *= al0;
+      o[i][2] *= al1;
+      o[i][3] *= al1;
     }
-  };
-  auto masks = [&](int st) { return *reinterpret_cast<const uint64_t*>(&sm.vmask[st][0]); };
+  }
+  const int pr = (lane & 7) + 8 * ((lane >> 3) & 1);
+  const uint32_t vb = v + pr * 1024 + 16 * kv4_vplace(16 * w + (lane >> 4), pr);
+  uint32_t pa[K4_BK / 16][4];
+#pragma unroll
+  for (int ks = 0; ks < K4_BK / 16; ++ks)
+    ldsm_x4(pbase + (pr * K4_PROW + 16 * ks + 8 * (lane >> 4)) * 2, pa[ks][0], pa[ks][1], pa[ks][2],
+            pa[ks][3]);
+#pragma unroll
+  for (int np = 0; np < 8; ++np) {
+    // pieces 16w + 2np (+ 1): the second eight lie 128 bytes on, their places turned by 1
+    const uint32_t va = np < 4 ? vb ^ (32u * np) : (vb ^ (32u * (np - 4) + 16u)) + 128u;
+#pragma unroll
+    for (int ks = 0; ks < K4_BK / 16; ++ks) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4_t(va + 16384u * ks, b0, b1, b2, b3);
+      mma_bf16(o[2 * np], pa[ks], b0, b1);
+      mma_bf16(o[2 * np + 1], pa[ks], b2, b3);
+    }
+  }
+}
+
+// The two groups take the tiles of an item in turn (group j those with index j mod 2) and
+// keep their own softmax state and O: while one waits for its softmax or barriers, the
+// other's products run.  At the item's end group 1 leaves its O in shared memory and
+// group 0 merges and stores.
+__device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
+  const int grp = threadIdx.x / K4_GTHREADS, tid = threadIdx.x % K4_GTHREADS;
+  const int warp = tid >> 5, lane = tid & 31;
+  Kv4Group& G = sm.grp[grp];
+  volatile int* abort = &sm.abort;
+  const int half = warp >> 1, part = warp & 1;  // QK: dim half, keys 16 part..+16
+  const int g = lane >> 2, cq = lane & 3;
+  const int sh = 4 * warp + (lane >> 3);  // softmax: head of this lane
+  const int sk = 4 * (lane & 7);          // and its four keys
+  const uint32_t vbase = smem_u32(&G.v[0][0]), pbase = smem_u32(&G.p[0][0]);
+  int stage = grp;
+  uint32_t ph = 0;
+  const long nj = attn_nitems(a);
   for (long it = 0; it < nj; ++it) {
     const AttnItem x = attn_item<K4_BK>(a, it);
     if (!mbar_wait(smem_u32(&sm.qfull), it & 1, abort, kErrTimeoutEpilogue)) return;
-    uint32_t qa[9][4];
-    {
-      // dims 128kq + 32cq + 4i..+4 of heads g, g + 8: the order in which kv4_qk expands
+    uint32_t qa[18][4];
+    // dims 256 half + 64cq + 8i..+8 of heads g, g + 8 in the pairs that e2m1_expand makes
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int ofs = (128 * kq + 32 * cq + 4 * i) * 2;
-        const uint2 u = *reinterpret_cast<const uint2*>(&sm.q[g][ofs]);
-        const uint2 v = *reinterpret_cast<const uint2*>(&sm.q[g + 8][ofs]);
-        qa[i][0] = u.x;
-        qa[i][1] = v.x;
-        qa[i][2] = u.y;
-        qa[i][3] = v.y;
+    for (int i = 0; i < 8; ++i) {
+      const int ofs = (256 * half + 64 * cq + 8 * i) * 2;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const uint4 u = *reinterpret_cast<const uint4*>(&sm.q[g + 8 * hh][ofs]);
+        qa[2 * i][hh] = __byte_perm(u.x, u.z, 0x5410);          // dims 0, 4
+        qa[2 * i][2 + hh] = __byte_perm(u.x, u.z, 0x7632);      // 1, 5
+        qa[2 * i + 1][hh] = __byte_perm(u.y, u.w, 0x5410);      // 2, 6
+        qa[2 * i + 1][2 + hh] = __byte_perm(u.y, u.w, 0x7632);  // 3, 7
       }
-      ldsm_x4(smem_u32(&sm.q[(lane & 7) + 8 * ((lane >> 3) & 1)][0]) +
-                  (AT_DV + 16 * kq + 8 * (lane >> 4)) * 2,
-              qa[8][0], qa[8][1], qa[8][2], qa[8][3]);
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      ldsm_x4(smem_u32(&sm.q[(lane & 7) + 8 * ((lane >> 3) & 1)][0]) +
+                  (AT_DV + 32 * half + 16 * i + 8 * (lane >> 4)) * 2,
+              qa[16 + i][0], qa[16 + i][1], qa[16 + i][2], qa[16 + i][3]);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.qempty));
-    float o[8][4];
+    float o[16][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m_run = -INFINITY, l_run = 0.f;  // softmax state of head sh (its 16 lanes agree)
+    for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m_run = -INFINITY, l_run = 0.f;  // softmax state of head sh (its 8 lanes agree)
 
-    if (!mbar_wait(smem_u32(&sm.full[stage]), ph, abort, kErrTimeoutEpilogue)) return;
-    int cur = stage, cur_last = sm.last[stage];
-    uint64_t cur_vm = masks(stage);
-    {
-      float c[4][4];
-      kv4_qk(&sm.raw[stage][0][0], qa, kq, kh, lane, c);
-      store_partial(c);
-    }
-    if (++stage == K4_STAGES) {
-      stage = 0;
-      ph ^= 1;
-    }
-    for (;;) {
-      named_bar_sync(1, AT_CONSUMERS);  // partials of cur complete, P V of prev done
-      if (tid == 0 && rel >= 0) mbar_arrive(smem_u32(&sm.empty[rel]));
-      const bool more = !cur_last;
-      float c[4][4];
-      int nxt = -1, nxt_last = 1;
-      uint64_t nxt_vm = 0;
-      if (more) {  // the next tile's QK runs under this tile's softmax
-        if (!mbar_wait(smem_u32(&sm.full[stage]), ph, abort, kErrTimeoutEpilogue)) return;
-        nxt = stage;
-        nxt_last = sm.last[stage];
-        nxt_vm = masks(stage);
-        kv4_qk(&sm.raw[stage][0][0], qa, kq, kh, lane, c);
-        if (++stage == K4_STAGES) {
-          stage = 0;
-          ph ^= 1;
+    for (bool last = false; !last;) {
+      if (!mbar_wait(smem_u32(&sm.full[stage]), ph, abort, kErrTimeoutEpilogue)) return;
+      last = sm.last[stage] != 0;
+      const uint32_t vm = *reinterpret_cast<const uint32_t*>(&sm.vmask[stage][0]);
+      if (vm) {
+        float c[2][4];
+        kv4_qk(sm.raw[stage], vbase, qa, half, part, lane, c);
+        float* sp = &G.s_part[half][0][0] + 16 * part + 2 * cq;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          *reinterpret_cast<float2*>(sp + g * K4_SROW + 8 * n) = make_float2(c[n][0], c[n][1]);
+          *reinterpret_cast<float2*>(sp + (g + 8) * K4_SROW + 8 * n) = make_float2(c[n][2], c[n][3]);
         }
       }
+      named_bar_sync(1 + grp, K4_GTHREADS);  // the tile is expanded, its partials complete
+      if (tid == 0) mbar_arrive(smem_u32(&sm.empty[stage]));
+      stage += K4_GROUPS;
+      if (stage >= K4_STAGES) {
+        stage = grp;
+        ph ^= 1;
+      }
+      if (!vm) continue;
       {
-        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 u = *reinterpret_cast<const float4*>(&G.s_part[0][sh][sk]);
+        const float4 w = *reinterpret_cast<const float4*>(&G.s_part[1][sh][sk]);
+        const unsigned vb = vm >> sk;
+        const float z0 = (vb & 1u) ? (u.x + w.x) * a.scale_log2 : -INFINITY;
+        const float z1 = (vb & 2u) ? (u.y + w.y) * a.scale_log2 : -INFINITY;
+        const float z2 = (vb & 4u) ? (u.z + w.z) * a.scale_log2 : -INFINITY;
+        const float z3 = (vb & 8u) ? (u.w + w.w) * a.scale_log2 : -INFINITY;
+        float t = fmaxf(fmaxf(z0, z1), fmaxf(z2, z3));
 #pragma unroll
-        for (int qq = 0; qq < 4; ++qq) {
-          const float4 u = *reinterpret_cast<const float4*>(&sm.s_part[qq][sh][sk]);
-          z.x += u.x;
-          z.y += u.y;
-          z.z += u.z;
-          z.w += u.w;
-        }
-        const unsigned vb = static_cast<unsigned>(cur_vm >> sk);
-        z.x = (vb & 1u) ? z.x * a.scale_log2 : -INFINITY;
-        z.y = (vb & 2u) ? z.y * a.scale_log2 : -INFINITY;
-        z.z = (vb & 4u) ? z.z * a.scale_log2 : -INFINITY;
-        z.w = (vb & 8u) ? z.w * a.scale_log2 : -INFINITY;
-        float t = fmaxf(fmaxf(z.x, z.y), fmaxf(z.z, z.w));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+        for (int off = 4; off > 0; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
         const float n = fmaxf(m_run, t);
         const float al = (n == -INFINITY) ? 1.f : fast_exp2(m_run - n);
         const float bse = (n == -INFINITY) ? 0.f : n;
-        const float e0 = fast_exp2(z.x - bse), e1 = fast_exp2(z.y - bse);
-        const float e2 = fast_exp2(z.z - bse), e3 = fast_exp2(z.w - bse);
-        float rs = (e0 + e1) + (e2 + e3);
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, off);
-        l_run = l_run * al + rs;
+        const float e0 = fast_exp2(z0 - bse), e1 = fast_exp2(z1 - bse);
+        const float e2 = fast_exp2(z2 - bse), e3 = fast_exp2(z3 - bse);
+        l_run = l_run * al + ((e0 + e1) + (e2 + e3));  // this lane's four keys' share
         m_run = n;
-        *reinterpret_cast<uint2*>(&sm.p[sh][sk]) = make_uint2(pack_bf16(e0, e1), pack_bf16(e2, e3));
-        if ((lane & 15) == 0) sm.alpha[sh] = al;
+        *reinterpret_cast<uint2*>(&G.p[sh][sk]) = make_uint2(pack_bf16(e0, e1), pack_bf16(e2, e3));
+        if ((lane & 7) == 0) G.alpha[sh] = al;
       }
-      named_bar_sync(1, AT_CONSUMERS);  // P, alpha complete
-      kv4_pv(&sm.raw[cur][0][0], smem_u32(&sm.p[0][0]), sm.alpha[g], sm.alpha[g + 8], warp, lane, o);
-      rel = cur;
-      if (!more) break;
-      store_partial(c);
-      cur = nxt;
-      cur_last = nxt_last;
-      cur_vm = nxt_vm;
+      named_bar_sync(1 + grp, K4_GTHREADS);  // P, alpha complete
+      kv4_pv(vbase, pbase, G.alpha[g], G.alpha[g + 8], warp, lane, o);
+      named_bar_sync(1 + grp, K4_GTHREADS);  // the expanded tile may be overwritten
     }
 
-    // ---- item epilogue: head h's final max and sum live in warp h/2
-    named_bar_sync(1, AT_CONSUMERS);  // every warp's P V of the item is done
-    if ((lane & 15) == 0) {
-      sm.fin_m[sh] = m_run;
-      sm.fin_l[sh] = l_run;
+    // ---- item epilogue
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, off);
+    if ((lane & 7) == 0) {
+      G.fin_m[sh] = m_run;
+      G.fin_l[sh] = l_run;
     }
-    named_bar_sync(1, AT_CONSUMERS);
-    // this lane holds dims 64 warp + 16cq..+16 of heads g (o[.][0..1]) and g + 8 (o[.][2..3])
+    // this lane holds dims 128 warp + 8j + cq and + cq + 4 of heads g (o[j][0..1]) and g + 8
+    // (o[j][2..3]); group 1 leaves them as four floats per (j, lane)
+    if (grp == 1) {
+      float4* dst = reinterpret_cast<float4*>(&G.v[0][0]) + warp * 512 + lane;
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int h = g + 8 * hh;
-      const float M = sm.fin_m[h], L = sm.fin_l[h];
-      const int d = 64 * warp + 16 * cq;
-      if (!a.split) {
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        uint32_t u[8];
+      for (int j = 0; j < 16; ++j) dst[32 * j] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
+    }
+    named_bar_sync(1 + K4_GROUPS, AT_CONSUMERS);
+    if (grp == 0) {
+      float wt0[2], wt1[2], M[2], L[2];  // heads g, g + 8: the groups' weights
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {  // dims 2i, 2i + 1 of the 16
-          const int j = 2 * (i & 3), n = 2 * hh + (i >> 2);
-          u[i] = pack_bf16(o[j][n] * inv, o[j + 1][n] * inv);
+      for (int hh = 0; hh < 2; ++hh) {
+        const int h = g + 8 * hh;
+        const float m0 = G.fin_m[h], m1 = sm.grp[1].fin_m[h];
+        M[hh] = fmaxf(m0, m1);
+        wt0[hh] = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M[hh]);
+        wt1[hh] = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M[hh]);
+        L[hh] = G.fin_l[h] * wt0[hh] + sm.grp[1].fin_l[h] * wt1[hh];
+        if (!a.split) {
+          const float inv = L[hh] > 0.f ? 1.f / L[hh] : 0.f;
+          wt0[hh] *= inv;
+          wt1[hh] *= inv;
         }
-        uint32_t* ob = reinterpret_cast<uint32_t*>(a.out + (x.qrow * AT_H + h) * AT_DV + d);
-        if ((reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
-          reinterpret_cast<uint4*>(ob)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-          reinterpret_cast<uint4*>(ob)[1] = make_uint4(u[4], u[5], u[6], u[7]);
-        } else {  // only required to be aligned to 4
+      }
+      const float4* other = reinterpret_cast<const float4*>(&sm.grp[1].v[0][0]) + warp * 512 + lane;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ob[i] = u[i];
-        }
-        if (a.lse && warp == 0 && cq == 0)
-          a.lse[x.qrow * AT_H + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
-      } else {
-        float* po = a.part_o + (x.pslot * AT_H + h) * AT_DV + d;
+      for (int j = 0; j < 16; ++j) {
+        const float4 u = other[32 * j];
+        const float r[4] = {o[j][0] * wt0[0] + u.x * wt1[0], o[j][1] * wt0[0] + u.y * wt1[0],
+                            o[j][2] * wt0[1] + u.z * wt1[1], o[j][3] * wt0[1] + u.w * wt1[1]};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // dims 4i..4i+3
-          const int j = 4 * (i & 1), n = 2 * hh + (i >> 1);
-          *reinterpret_cast<float4*>(po + 4 * i) =
-              make_float4(o[j][n], o[j + 1][n], o[j + 2][n], o[j + 3][n]);
+        for (int hh = 0; hh < 2; ++hh) {
+          const int h = g + 8 * hh, d = 128 * warp + 8 * j;
+          if (!a.split) {
+            // trade one value with the neighbour: even lanes then hold dims cq, cq + 1, odd
+            // ones cq + 3, cq + 4
+            const float got = __shfl_xor_sync(0xffffffffu, (cq & 1) ? r[2 * hh] : r[2 * hh + 1], 1);
+            *reinterpret_cast<uint32_t*>(a.out + (x.qrow * AT_H + h) * AT_DV + d +
+                                         ((cq & 1) ? cq + 3 : cq)) =
+                (cq & 1) ? pack_bf16(got, r[2 * hh + 1]) : pack_bf16(r[2 * hh], got);
+          } else {
+            float* po = a.part_o + (x.pslot * AT_H + h) * AT_DV + d + cq;
+            po[0] = r[2 * hh];
+            po[4] = r[2 * hh + 1];
+          }
         }
-        if (warp == 0 && cq == 0) {
-          a.part_ml[(x.pslot * AT_H + h) * 2] = M;
-          a.part_ml[(x.pslot * AT_H + h) * 2 + 1] = L;
+      }
+      if (warp == 0 && cq == 0) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int h = g + 8 * hh;
+          if (a.split) {
+            a.part_ml[(x.pslot * AT_H + h) * 2] = M[hh];
+            a.part_ml[(x.pslot * AT_H + h) * 2 + 1] = L[hh];
+          } else if (a.lse) {
+            a.lse[x.qrow * AT_H + h] =
+                L[hh] > 0.f ? (M[hh] + log2f(L[hh])) * 0.69314718055994531f : -INFINITY;
+          }
         }
       }
     }
+    named_bar_sync(1 + K4_GROUPS, AT_CONSUMERS);  // group 1's tile and sums have been read
   }
 }
 
@@ -470,10 +527,13 @@ __global__ void __launch_bounds__(K4_THREADS, 1)
   }
   __syncthreads();
   grid_dep_wait();  // set-up above touches no global memory
-  if (threadIdx.x >= AT_CONSUMERS)
+  if (threadIdx.x >= AT_CONSUMERS) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K4_PREGS));
     kv4_producer(sm, a, pg);
-  else
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K4_CREGS));
     kv4_consumer(sm, a);
+  }
   __syncthreads();
 }
 
