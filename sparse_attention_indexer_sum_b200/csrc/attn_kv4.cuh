@@ -23,11 +23,10 @@
 // 3 x 341 queries of 2048 rows, its integer pipe the limit at 2300 cycles per 32 keys).
 
 constexpr int K4_BK = 32;                       // keys per tile
-constexpr int K4_STAGES = 6;                    // even: a stage always serves one group
+constexpr int K4_STAGES = 8;                    // a stage always serves one group and one producer
 constexpr int K4_GROUPS = 2;
 constexpr int K4_GTHREADS = AT_CONSUMERS / K4_GROUPS;
 constexpr int K4_PROD_WARPS = 4;
-constexpr int K4_PROD_ROWS = K4_BK / K4_PROD_WARPS;  // rows of a tile that each copies
 constexpr int K4_THREADS = AT_CONSUMERS + 32 * K4_PROD_WARPS;
 // Registers per thread after the roles part: the block starts with 168 each (64512 in
 // all), the producers give up theirs above K4_PREGS and the consumers take K4_CREGS.
@@ -39,16 +38,18 @@ constexpr int K4_CHUNKS = KV4_ROW_BYTES / 16;   // 16-byte copies per row
 constexpr int K4_SROW = K4_BK + 8;              // padded partial-score row (floats)
 constexpr int K4_PROW = K4_BK + 8;              // padded P row (bf16)
 constexpr int K4_RROW = 144;                    // padded rope row (bytes)
-static_assert(K4_STAGES % K4_GROUPS == 0 && K4_CHUNKS <= 32, "stages per group, lanes per row");
+static_assert(K4_STAGES % K4_GROUPS == 0 && K4_STAGES % K4_PROD_WARPS == 0 &&
+                  K4_PROD_WARPS % K4_GROUPS == 0 && K4_CHUNKS <= 32 && K4_BK == 32,
+              "every use of a stage falls to one group and one producer; a lane per row");
 
 struct Kv4Stage {
-  uint8_t codes[K4_BK][256];  // 16-byte piece i of row r at place i ^ (r & 1)
+  uint8_t codes[K4_BK][256];  // 16-byte piece i of row r at place i ^ 4 (r & 1)
   uint8_t rope[K4_BK][K4_RROW];
   uint8_t scale[K4_BK][16];
 };
 struct Kv4Group {  // one consumer group's own
   alignas(128) uint8_t v[K4_BK][1024];  // its expanded tile (kv4_vplace); at an item's end its O
-  alignas(16) float s_part[2][AT_H][K4_SROW];
+  alignas(16) float s_part[4][AT_H][K4_SROW];  // partial scores of the dim quarters
   alignas(16) __nv_bfloat16 p[AT_H][K4_PROW];
   float alpha[AT_H];
   float fin_m[AT_H], fin_l[AT_H];
@@ -59,7 +60,7 @@ struct Kv4Smem {
   Kv4Group grp[K4_GROUPS];
   alignas(128) uint8_t q[AT_H][AT_ROWB];
   alignas(16) int ibuf[2][AT_MAXK];
-  alignas(4) uint8_t vmask[K4_STAGES][K4_PROD_WARPS];  // bit j of [w]: row 8w + j has an entry
+  uint32_t vmask[K4_STAGES];  // bit j: row j has an entry
   int last[K4_STAGES];
   alignas(8) uint64_t full[K4_STAGES];
   uint64_t empty[K4_STAGES];
@@ -81,8 +82,8 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Producers walk the items as attn_producer's do; warp pw copies rows 8pw..8pw+7 of
-// every tile, lane l < 25 the row's 16-byte piece l.
+// Producers walk the items as attn_producer's do; every fourth tile is one warp's: lane l
+// looks up row l of the tile, then lane l < 25 copies the 16-byte piece l of every row.
 __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, const PagedArgs& pg) {
   const int lane = threadIdx.x & 31;
   const int pw = (threadIdx.x - AT_CONSUMERS) >> 5;
@@ -92,7 +93,7 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
   uint32_t at0, at1, step;
   if (lane < 16) {
     at0 = offsetof(Kv4Stage, codes) + 16 * lane;
-    at1 = offsetof(Kv4Stage, codes) + 16 * (lane ^ 1);
+    at1 = offsetof(Kv4Stage, codes) + 16 * (lane ^ 4);
     step = 256;
   } else if (lane == 16) {
     at0 = at1 = offsetof(Kv4Stage, scale);
@@ -101,10 +102,11 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
     at0 = at1 = offsetof(Kv4Stage, rope) + 16 * (lane - 17);
     step = K4_RROW;
   }
-  at0 += smem_u32(&sm.raw[0]) + K4_PROD_ROWS * pw * step;
-  at1 += smem_u32(&sm.raw[0]) + K4_PROD_ROWS * pw * step;
+  at0 += smem_u32(&sm.raw[0]);
+  at1 += smem_u32(&sm.raw[0]);
   const uint8_t* src0 = reinterpret_cast<const uint8_t*>(a.kv) + 16 * lane;
-  int stage = 0, ib = 0, qloads = 0;
+  int stage = pw, ib = 0, qloads = 0;
+  int t0 = pw;  // this warp's first tile of the item (its tiles of all items: every fourth)
   uint32_t ph = 0, iph[2] = {0u, 0u};
   int ipending[2] = {0, 0};
   const long nj = attn_nitems(a);
@@ -160,28 +162,28 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
                  smem_u32(&sm.qfull));
       ++qloads;
     }
-    // the pool row of row (8pw + lane mod 8) of tile t, read one tile ahead
+    // the pool row of row `lane` of tile t
     auto pool_row = [&](int t) -> int {
-      const int j = t * K4_BK + K4_PROD_ROWS * pw + (lane & (K4_PROD_ROWS - 1));
+      const int j = t * K4_BK + lane;
       const int s = (t < ntiles && j < cnt) ? ilist[j] : -1;
       if (!in_bounds(s >= -1 && s < len, kErrBoundsGather) || s < 0 || s >= len) return -1;
       return static_cast<int>(attn_page_row(pg, b, s));
     };
     // the groups take turns: an even number of tiles, at least two
     const int nt = ntiles > 2 ? (ntiles + 1) & ~1 : 2;
-    int prow = pool_row(0), pnext = pool_row(1);
+    int prow = pool_row(t0);
     bool ok = true;
-    for (int t = 0; t < nt; ++t) {
-      const int pnext2 = pool_row(t + 2);
+    for (int t = t0; t < nt; t += K4_PROD_WARPS) {
+      const int pnext = pool_row(t + K4_PROD_WARPS);
       if (!mbar_wait(smem_u32(&sm.empty[stage]), ph ^ 1, abort, kErrTimeoutProducer)) {
         ok = false;
         break;
       }
-      const unsigned valid = __ballot_sync(0xffffffffu, prow >= 0) & ((1u << K4_PROD_ROWS) - 1u);
+      const uint32_t valid = __ballot_sync(0xffffffffu, prow >= 0);
       const uint32_t so = stage * static_cast<uint32_t>(sizeof(Kv4Stage));
       if (t < ntiles) {  // a tile without entries is not looked at
 #pragma unroll
-        for (int r = 0; r < K4_PROD_ROWS; ++r) {
+        for (int r = 0; r < K4_BK; ++r) {
           const int row = __shfl_sync(0xffffffffu, prow, r);
           if (lane < K4_CHUNKS)
             cp_async16(((r & 1) ? at1 : at0) + so + r * step,
@@ -191,17 +193,19 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
       const uint32_t fb = smem_u32(&sm.full[stage]);
       cp_async_arrive(fb);
       if (lane == 0) {
-        sm.vmask[stage][pw] = static_cast<uint8_t>(valid);
-        if (pw == 0) sm.last[stage] = t >= nt - K4_GROUPS;
+        sm.vmask[stage] = valid;
+        sm.last[stage] = t >= nt - K4_GROUPS;
         mbar_arrive(fb);
       }
       prow = pnext;
-      pnext = pnext2;
-      if (++stage == K4_STAGES) {
-        stage = 0;
+      stage += K4_PROD_WARPS;
+      if (stage >= K4_STAGES) {
+        stage = pw;
         ph ^= 1;
       }
     }
+    // the next item's first tile of this warp: the tiles of all items are dealt in turn
+    t0 = (t0 - nt) & (K4_PROD_WARPS - 1);
     if (!ok) break;
   }
   // no copy is in flight when the CTA ends
@@ -232,77 +236,88 @@ __device__ __forceinline__ void e2m1_expand(uint32_t w, uint32_t s, uint32_t* o)
   o[3] = bf16x2_mul(((w8 & 0x00F000F0u) * 0x0104u) & kMask, s);
 }
 
-// Place (in 16-byte pieces) of piece L (0..63) of key r in its 1024-byte row of the
-// expanded tile.  The stores of a quad's lanes go to pieces 8 apart, of two keys at a
-// time; the transposed loads take one piece of eight consecutive keys.
-__device__ __forceinline__ int kv4_vplace(int L, int r) {
-  return L ^ ((L >> 3) & 3) ^ ((r & 1) << 2) ^ ((r >> 1) & 3);
+// D = A B (mma_bf16 with nothing to add to).
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Expands the codes of this warp's share of a tile into the bf16 tile at v (a shared
-// address) and multiplies them with Q: dims 256 half..+256 and rope dims 32 half..+32 of
-// keys 16 part..+16 (lane: keys g and g + 8 of them, two blocks of dims).
-__device__ __forceinline__ void kv4_qk(const Kv4Stage& raw, uint32_t v,
-                                       const uint32_t (&qa)[18][4], int half, int part, int lane,
-                                       float (&c)[2][4]) {
-  const int g = lane >> 2, cq = lane & 3, r = 16 * part + g;
-  const int blk = 8 * half + 2 * cq;
-  uint32_t e2[2];
+// Place (in 16-byte pieces) of piece L (0..63) of key r in its 1024-byte row of the
+// expanded tile.  A store's eight lanes take pieces 4 apart of two neighbouring keys, a
+// transposed load one piece of eight consecutive keys: both find all banks.
+__device__ __forceinline__ int kv4_vplace(int L, int r) {
+  return L ^ ((L >> 3) & 1) ^ ((r & 1) << 1) ^ ((r >> 1) & 1) ^ (r & 4);
+}
+
+// Expands the codes of this warp's quarter of a tile into the bf16 tile at v and multiplies
+// them with Q: dims 128 kq..+128 and rope dims 16 kq..+16 of all keys (lane: keys
+// g + 8n, block 4 kq + cq).  The partial scores go to sp, the quarter's rows of heads.
+// e[n]: the scale code of the lane's block of key g + 8n.  BIG: some scale code of the
+// warp is above 128, so that 2^(E - 1) is no bf16 and the factor goes in two steps.
+template <bool BIG>
+__device__ __forceinline__ void kv4_qk(const Kv4Stage& raw, uint8_t* v, const uint32_t (&qa)[9][4],
+                                       int kq, int lane, const uint32_t (&e)[4], float* sp) {
+  const int g = lane >> 2, cq = lane & 3, blk = 4 * kq + cq;
+  // piece i of the block has place (4 blk + i) ^ x: x as in kv4_vplace, the same for g + 8n
+  const uint32_t vb = g * 1024 + 16 * kv4_vplace(4 * blk, g);
+  uint32_t w[4][4], s[4], s2[4];
+  float c[4][4];
 #pragma unroll
-  for (int n = 0; n < 2; ++n)
-    e2[n] = *reinterpret_cast<const uint16_t*>(&raw.scale[r + 8 * n][blk]);
-  // 2^(E - 1) as bf16 needs E <= 128: larger scales (and NaN) are finished below
-  const bool big = __any_sync(0xffffffffu, max(max(e2[0] & 0xFFu, e2[0] >> 8),
-                                               max(e2[1] & 0xFFu, e2[1] >> 8)) > 128u);
-  // the pieces 8m..8m+7 (m = 4 half + cq) of rows r and r + 8 have places 8m + (i ^ x)
-  const uint32_t vb = v + r * 1024 + 16 * kv4_vplace(4 * blk, r);
-  float d[2][4];
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-    d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.f;
+  for (int n = 0; n < 4; ++n) {
+    const uint4 u =
+        *reinterpret_cast<const uint4*>(&raw.codes[g + 8 * n][16 * (blk ^ ((g & 1) << 2))]);
+    w[n][0] = u.x;
+    w[n][1] = u.y;
+    w[n][2] = u.z;
+    w[n][3] = u.w;
+    s[n] = ((BIG && e[n] > 128u ? 128u : e[n]) + 126u) * 0x00800080u;
+    if constexpr (BIG)  // the rest of larger scales: 2^(E - 128), or NaN
+      s2[n] = e[n] == 255u ? 0x7FFF7FFFu
+                           : ((e[n] > 128u ? e[n] - 128u : 0u) + 127u) * 0x00800080u;
   }
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int i = 0; i < 4; ++i) {
+    uint32_t o[4][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint4 w =
-          *reinterpret_cast<const uint4*>(&raw.codes[r + 8 * n][16 * ((blk + u) ^ (r & 1))]);
-      const uint32_t e = (e2[n] >> (8 * u)) & 0xFFu;
-      const uint32_t s = ((e < 128u ? e : 128u) + 126u) * 0x00800080u;
-      uint32_t o[16];
-      e2m1_expand(w.x, s, o);
-      e2m1_expand(w.y, s, o + 4);
-      e2m1_expand(w.z, s, o + 8);
-      e2m1_expand(w.w, s, o + 12);
-      if (big) {  // the rest of larger scales: 2^(E - 128), or NaN
-        const uint32_t s2 =
-            e == 255u ? 0x7FFF7FFFu : ((e > 128u ? e - 128u : 0u) + 127u) * 0x00800080u;
+    for (int n = 0; n < 4; ++n) {
+      e2m1_expand(w[n][i], s[n], o[n]);
+      if constexpr (BIG) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = bf16x2_mul(o[i], s2);
+        for (int j = 0; j < 4; ++j) o[n][j] = bf16x2_mul(o[n][j], s2[n]);
       }
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        mma_bf16(c[n], qa[8 * u + 2 * i], o[4 * i], o[4 * i + 1]);
-        mma_bf16(d[n], qa[8 * u + 2 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      }
+    for (int n = 0; n < 4; ++n) {
+      if (i == 0)
+        mma_bf16_first(c[n], qa[0], o[n][0], o[n][1]);
+      else
+        mma_bf16(c[n], qa[2 * i], o[n][0], o[n][1]);
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                         (vb ^ (16u * (4 * u + i))) + 8192u * n),
-                     "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
-                     : "memory");
+    for (int n = 0; n < 4; ++n) {
+      mma_bf16(c[n], qa[2 * i + 1], o[n][2], o[n][3]);
+      *reinterpret_cast<uint4*>(v + ((vb ^ (16u * i)) + 8192u * n)) =
+          make_uint4(o[n][0], o[n][1], o[n][2], o[n][3]);
     }
   }
+  const uint32_t rope = smem_u32(&raw.rope[(lane & 7) + 8 * (lane >> 4)][0]) + 32 * kq +
+                        16 * ((lane >> 3) & 1);
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
+  for (int n = 0; n < 4; n += 2) {
     uint32_t b0, b1, b2, b3;
-    ldsm_x4(smem_u32(&raw.rope[16 * part + 8 * n + (lane & 7)][64 * half + 16 * (lane >> 3)]), b0,
-            b1, b2, b3);
-    mma_bf16(c[n], qa[16], b0, b1);
-    mma_bf16(d[n], qa[17], b2, b3);
+    ldsm_x4(rope + 8 * n * K4_RROW, b0, b1, b2, b3);
+    mma_bf16(c[n], qa[8], b0, b1);
+    mma_bf16(c[n + 1], qa[8], b2, b3);
+  }
+  float* p = sp + 2 * cq;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[n][i] += d[n][i];
+  for (int n = 0; n < 4; ++n) {
+    *reinterpret_cast<float2*>(p + g * K4_SROW + 8 * n) = make_float2(c[n][0], c[n][1]);
+    *reinterpret_cast<float2*>(p + (g + 8) * K4_SROW + 8 * n) = make_float2(c[n][2], c[n][3]);
   }
 }
 
@@ -327,11 +342,11 @@ __device__ __forceinline__ void kv4_pv(uint32_t v, uint32_t pbase, float al0, fl
     ldsm_x4(pbase + (pr * K4_PROW + 16 * ks + 8 * (lane >> 4)) * 2, pa[ks][0], pa[ks][1], pa[ks][2],
             pa[ks][3]);
 #pragma unroll
-  for (int np = 0; np < 8; ++np) {
-    // pieces 16w + 2np (+ 1): the second eight lie 128 bytes on, their places turned by 1
-    const uint32_t va = np < 4 ? vb ^ (32u * np) : (vb ^ (32u * (np - 4) + 16u)) + 128u;
+  for (int ks = 0; ks < K4_BK / 16; ++ks) {  // all dims of 16 keys: independent products
 #pragma unroll
-    for (int ks = 0; ks < K4_BK / 16; ++ks) {
+    for (int np = 0; np < 8; ++np) {
+      // pieces 16w + 2np (+ 1): the second eight lie 128 bytes on, their places turned by 1
+      const uint32_t va = np < 4 ? vb ^ (32u * np) : (vb ^ (32u * (np - 4) + 16u)) + 128u;
       uint32_t b0, b1, b2, b3;
       ldsm_x4_t(va + 16384u * ks, b0, b1, b2, b3);
       mma_bf16(o[2 * np], pa[ks], b0, b1);
@@ -349,7 +364,6 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
   const int warp = tid >> 5, lane = tid & 31;
   Kv4Group& G = sm.grp[grp];
   volatile int* abort = &sm.abort;
-  const int half = warp >> 1, part = warp & 1;  // QK: dim half, keys 16 part..+16
   const int g = lane >> 2, cq = lane & 3;
   const int sh = 4 * warp + (lane >> 3);  // softmax: head of this lane
   const int sk = 4 * (lane & 7);          // and its four keys
@@ -360,11 +374,11 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
   for (long it = 0; it < nj; ++it) {
     const AttnItem x = attn_item<K4_BK>(a, it);
     if (!mbar_wait(smem_u32(&sm.qfull), it & 1, abort, kErrTimeoutEpilogue)) return;
-    uint32_t qa[18][4];
-    // dims 256 half + 64cq + 8i..+8 of heads g, g + 8 in the pairs that e2m1_expand makes
+    uint32_t qa[9][4];
+    // dims 128 warp + 32cq + 8i..+8 of heads g, g + 8 in the pairs that e2m1_expand makes
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ofs = (256 * half + 64 * cq + 8 * i) * 2;
+    for (int i = 0; i < 4; ++i) {
+      const int ofs = (128 * warp + 32 * cq + 8 * i) * 2;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const uint4 u = *reinterpret_cast<const uint4*>(&sm.q[g + 8 * hh][ofs]);
@@ -374,13 +388,12 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
         qa[2 * i + 1][2 + hh] = __byte_perm(u.y, u.w, 0x7632);  // 3, 7
       }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      ldsm_x4(smem_u32(&sm.q[(lane & 7) + 8 * ((lane >> 3) & 1)][0]) +
-                  (AT_DV + 32 * half + 16 * i + 8 * (lane >> 4)) * 2,
-              qa[16 + i][0], qa[16 + i][1], qa[16 + i][2], qa[16 + i][3]);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sm.qempty));
+    ldsm_x4(smem_u32(&sm.q[(lane & 7) + 8 * ((lane >> 3) & 1)][0]) +
+                (AT_DV + 16 * warp + 8 * (lane >> 4)) * 2,
+            qa[8][0], qa[8][1], qa[8][2], qa[8][3]);
+    // Q's place is given back once these loads have certainly returned: after the first
+    // tile whose products used them
+    bool qheld = true;
     float o[16][4];
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -389,19 +402,24 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
     for (bool last = false; !last;) {
       if (!mbar_wait(smem_u32(&sm.full[stage]), ph, abort, kErrTimeoutEpilogue)) return;
       last = sm.last[stage] != 0;
-      const uint32_t vm = *reinterpret_cast<const uint32_t*>(&sm.vmask[stage][0]);
+      const uint32_t vm = sm.vmask[stage];
       if (vm) {
-        float c[2][4];
-        kv4_qk(sm.raw[stage], vbase, qa, half, part, lane, c);
-        float* sp = &G.s_part[half][0][0] + 16 * part + 2 * cq;
+        const Kv4Stage& raw = sm.raw[stage];
+        uint32_t e[4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          *reinterpret_cast<float2*>(sp + g * K4_SROW + 8 * n) = make_float2(c[n][0], c[n][1]);
-          *reinterpret_cast<float2*>(sp + (g + 8) * K4_SROW + 8 * n) = make_float2(c[n][2], c[n][3]);
-        }
+        for (int n = 0; n < 4; ++n) e[n] = raw.scale[g + 8 * n][4 * warp + cq];
+        float* sp = &G.s_part[warp][0][0];
+        if (__any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > 128u))
+          kv4_qk<true>(raw, &G.v[0][0], qa, warp, lane, e, sp);
+        else
+          kv4_qk<false>(raw, &G.v[0][0], qa, warp, lane, e, sp);
       }
       named_bar_sync(1 + grp, K4_GTHREADS);  // the tile is expanded, its partials complete
-      if (tid == 0) mbar_arrive(smem_u32(&sm.empty[stage]));
+      if (tid == 0) {
+        mbar_arrive(smem_u32(&sm.empty[stage]));
+        if (vm && qheld) mbar_arrive(smem_u32(&sm.qempty));
+      }
+      if (vm) qheld = false;
       stage += K4_GROUPS;
       if (stage >= K4_STAGES) {
         stage = grp;
@@ -409,23 +427,36 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
       }
       if (!vm) continue;
       {
-        const float4 u = *reinterpret_cast<const float4*>(&G.s_part[0][sh][sk]);
-        const float4 w = *reinterpret_cast<const float4*>(&G.s_part[1][sh][sk]);
-        const unsigned vb = vm >> sk;
-        const float z0 = (vb & 1u) ? (u.x + w.x) * a.scale_log2 : -INFINITY;
-        const float z1 = (vb & 2u) ? (u.y + w.y) * a.scale_log2 : -INFINITY;
-        const float z2 = (vb & 4u) ? (u.z + w.z) * a.scale_log2 : -INFINITY;
-        const float z3 = (vb & 8u) ? (u.w + w.w) * a.scale_log2 : -INFINITY;
-        float t = fmaxf(fmaxf(z0, z1), fmaxf(z2, z3));
+        float4 u = *reinterpret_cast<const float4*>(&G.s_part[0][sh][sk]);
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-        const float n = fmaxf(m_run, t);
-        const float al = (n == -INFINITY) ? 1.f : fast_exp2(m_run - n);
-        const float bse = (n == -INFINITY) ? 0.f : n;
+        for (int qq = 1; qq < 4; ++qq) {
+          const float4 w = *reinterpret_cast<const float4*>(&G.s_part[qq][sh][sk]);
+          u.x += w.x;
+          u.y += w.y;
+          u.z += w.z;
+          u.w += w.w;
+        }
+        const unsigned vb = vm >> sk;
+        const float z0 = (vb & 1u) ? u.x * a.scale_log2 : -INFINITY;
+        const float z1 = (vb & 2u) ? u.y * a.scale_log2 : -INFINITY;
+        const float z2 = (vb & 4u) ? u.z * a.scale_log2 : -INFINITY;
+        const float z3 = (vb & 8u) ? u.w * a.scale_log2 : -INFINITY;
+        // the reference point moves only when a score exceeds it by more than 2^8 in the
+        // numerators: their sums have ample room, and most tiles then need no maximum
+        // over the head's lanes and no rescaling of O
+        float t = fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)), al = 1.f;
+        if (__any_sync(0xffffffffu, t > m_run + 8.f)) {
+#pragma unroll
+          for (int off = 4; off > 0; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+          const float n = fmaxf(m_run, t);
+          al = (n == -INFINITY) ? 1.f : fast_exp2(m_run - n);
+          l_run *= al;
+          m_run = n;
+        }
+        const float bse = (m_run == -INFINITY) ? 0.f : m_run;
         const float e0 = fast_exp2(z0 - bse), e1 = fast_exp2(z1 - bse);
         const float e2 = fast_exp2(z2 - bse), e3 = fast_exp2(z3 - bse);
-        l_run = l_run * al + ((e0 + e1) + (e2 + e3));  // this lane's four keys' share
-        m_run = n;
+        l_run += (e0 + e1) + (e2 + e3);  // this lane's four keys' share
         *reinterpret_cast<uint2*>(&G.p[sh][sk]) = make_uint2(pack_bf16(e0, e1), pack_bf16(e2, e3));
         if ((lane & 7) == 0) G.alpha[sh] = al;
       }
@@ -435,6 +466,7 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
     }
 
     // ---- item epilogue
+    if (qheld && tid == 0) mbar_arrive(smem_u32(&sm.qempty));
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, off);
     if ((lane & 7) == 0) {
@@ -513,12 +545,12 @@ __global__ void __launch_bounds__(K4_THREADS, 1)
       (reinterpret_cast<uintptr_t>(at_smem_raw) + 127) & ~static_cast<uintptr_t>(127));
   if (threadIdx.x == 0) {
     for (int s = 0; s < K4_STAGES; ++s) {
-      // every producer thread's copies, and one arrival per warp after its flags
-      mbar_init(smem_u32(&sm.full[s]), 32 * K4_PROD_WARPS + K4_PROD_WARPS);
+      // the copies of one producer warp's threads, and its arrival after the flags
+      mbar_init(smem_u32(&sm.full[s]), 32 + 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
     mbar_init(smem_u32(&sm.qfull), 1);
-    mbar_init(smem_u32(&sm.qempty), AT_CONSUMERS / 32);
+    mbar_init(smem_u32(&sm.qempty), K4_GROUPS);
     mbar_init(smem_u32(&sm.ifull[0]), 1);
     mbar_init(smem_u32(&sm.ifull[1]), 1);
     mbar_init(smem_u32(&sm.pitem), K4_PROD_WARPS);
