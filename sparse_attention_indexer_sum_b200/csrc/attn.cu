@@ -702,9 +702,8 @@ __device__ __forceinline__ void attn_consumer(AttnSmem& sm, const AttnArgs& a) {
 template <int FMT, int ADDR>
 __global__ void __launch_bounds__(AT_THREADS, 1)
     attn_mla_kernel(const AttnArgs a, const __grid_constant__ AttnAddrParam<ADDR> sg) {
-  extern __shared__ uint8_t at_smem_raw[];
-  AttnSmem& sm = *reinterpret_cast<AttnSmem*>(
-      (reinterpret_cast<uintptr_t>(at_smem_raw) + 127) & ~static_cast<uintptr_t>(127));
+  extern __shared__ __align__(128) uint8_t at_smem[];
+  AttnSmem& sm = *reinterpret_cast<AttnSmem*>(at_smem);
   if (threadIdx.x == 0) {
     for (int s = 0; s < AT_STAGES; ++s) {
       mbar_init(smem_u32(&sm.full[s]), AT_PRODUCERS);

@@ -5,22 +5,37 @@
 // dims.  Gathering it moves a third of a bf16 row's bytes, so what bounds this kernel is
 // no longer the gather but turning codes into operands of the warp-level MMA and moving
 // those through shared memory:
-//   * producer warps copy the raw rows with 16-byte cp.async (a row needs 25, which a
-//     warp issues for several rows at once); rows without an entry become zeros;
-//   * the eight consumer warps expand every code once, in the registers that feed QK:
-//     warp (half, group) covers dims 256 half..+256 of keys 8 group..+8.  The
-//     contraction's order of dims is free, so a lane takes 64 consecutive dims -- two
-//     blocks, two scales -- of its key with two 16-byte loads, and Q's fragments are
-//     loaded in the same order.  The expanded dims also go to a bf16 tile, swizzled so
-//     that neither these stores nor PV's transposed loads meet bank conflicts;
-//   * PV reads that tile; the order of the eight dims in each of its 16-byte pieces is
-//     the one the expansion leaves, undone when O is stored.
+//   * producer warps copy the raw rows with 16-byte cp.async (a row needs 25; a warp takes
+//     a whole tile of 32 rows); rows without an entry become zeros;
+//   * the eight consumer warps form two groups that take an item's tiles in turn, each with
+//     its own softmax state and O: one group's products fill the other's waits;
+//   * a warp owns 128 latent dims (and 16 rope dims) of its group's tile in QK and in PV.
+//     It expands its codes once, in registers: a lane takes one block, and so one scale, of
+//     four keys with four 16-byte loads (the contraction's order of dims is free, Q's
+//     fragments are loaded in the same order).  For PV the expanded registers are turned by
+//     movmatrix into operands with the keys along K: nothing of V goes back to shared
+//     memory;
+//   * the quarters' partial scores meet in shared memory, where the softmax of each head is
+//     computed once.  Its reference point moves only when a score exceeds it by 2^8.
 // Expansion: a code s e e m, its sign at bit 15 and e e m at bits 8..6, is the bf16
 // number value * 2^-126 (0.5 becomes a subnormal); one AND, one multiplication (both
 // shifts at once) and one AND move two codes, and a bf16 multiplication by 2^(E - 1)
-// gives two exact scaled values.  That is half integer-pipe work of a byte-permute table
-// (which with a second expansion for PV instead of the bf16 tile measured 561 us on
-// 3 x 341 queries of 2048 rows, its integer pipe the limit at 2300 cycles per 32 keys).
+// gives two exact scaled values.
+//
+// Measured on 3 x 341 queries of 2048 rows of 40000 (2.1 M rows, 7.3e13 flop; L2 holds the
+// cache): 392 us = 187 TFLOP/s, 0.11 of the measured bf16 rate, where the bf16 rows take
+// 400 us in attn_mla_kernel; 64 decode queries over 64 x 200000 rows: 32 us and 6 us for the
+// merge (52 MB of rows, 8 us at the measured HBM rate).  A tile of 32 keys costs an SM 1600
+// cycles; its products alone are 68 x 9 cycles of each tensor pipe (the warp-level MMA at M =
+// 16 heads) and its expansion 600 of each integer pipe, but a warp's chain of load, expand,
+// multiply, exchange, softmax, multiply is 2300 cycles long, and two groups overlap it only in
+// part (registers allow no third: V, O and Q take 164 of a thread's 216).
+// Earlier forms, on the same case: expansion by the producers into bf16 rows for the bf16
+// kernel's consumers 875 us; byte-permute tables and a second expansion for PV 561 us (integer
+// pipe); eight warps in step with a swizzled bf16 tile for PV 638 us; that tile with two
+// groups 474 us, with dim quarters 434 us, without generic addresses 401 us, and without the
+// barrier that its exchange between warps needed 396 us; sixteen consumer warps (104 registers,
+// spilled) 605 us; PV of a tile and QK of the next in one stretch 457 us.
 
 constexpr int K4_BK = 32;                       // keys per tile
 constexpr int K4_STAGES = 8;                    // a stage always serves one group and one producer
@@ -48,17 +63,16 @@ struct Kv4Stage {
   uint8_t scale[K4_BK][16];
 };
 struct Kv4Group {  // one consumer group's own
-  alignas(128) uint8_t v[K4_BK][1024];  // its expanded tile (kv4_vplace); at an item's end its O
   alignas(16) float s_part[4][AT_H][K4_SROW];  // partial scores of the dim quarters
   alignas(16) __nv_bfloat16 p[AT_H][K4_PROW];
   float alpha[AT_H];
   float fin_m[AT_H], fin_l[AT_H];
 };
-static_assert(sizeof(Kv4Group::v) == AT_H * AT_DV * sizeof(float), "O of an item fits the tile");
 struct Kv4Smem {
   alignas(128) Kv4Stage raw[K4_STAGES];
   Kv4Group grp[K4_GROUPS];
   alignas(128) uint8_t q[AT_H][AT_ROWB];
+  alignas(16) float4 o1[AT_H * AT_DV / 4];  // group 1's O at an item's end
   alignas(16) int ibuf[2][AT_MAXK];
   uint32_t vmask[K4_STAGES];  // bit j: row j has an entry
   int last[K4_STAGES];
@@ -246,64 +260,58 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Place (in 16-byte pieces) of piece L (0..63) of key r in its 1024-byte row of the
-// expanded tile.  A store's eight lanes take pieces 4 apart of two neighbouring keys, a
-// transposed load one piece of eight consecutive keys: both find all banks.
-__device__ __forceinline__ int kv4_vplace(int L, int r) {
-  return L ^ ((L >> 3) & 1) ^ ((r & 1) << 1) ^ ((r >> 1) & 1) ^ (r & 4);
+// The 8 x 8 transpose of a matrix of 16-bit values held two a lane (row lane / 4).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
-// Expands the codes of this warp's quarter of a tile into the bf16 tile at v and multiplies
-// them with Q: dims 128 kq..+128 and rope dims 16 kq..+16 of all keys (lane: keys
-// g + 8n, block 4 kq + cq).  The partial scores go to sp, the quarter's rows of heads.
-// e[n]: the scale code of the lane's block of key g + 8n.  BIG: some scale code of the
-// warp is above 128, so that 2^(E - 1) is no bf16 and the factor goes in two steps.
+// Expands the codes of this warp's quarter of a tile into v and multiplies them with Q:
+// dims 128 kq..+128 and rope dims 16 kq..+16 of all keys (lane: keys g + 8n, block
+// 4 kq + cq).  v[n][4i]: the codes of the block's dims 8i..8i+7, which become v[n][4i + j]:
+// dims 8i + j and 8i + j + 4 in bf16.  The partial scores
+// go to sp, the quarter's rows of heads.  e[n]: the scale code of the lane's block of key
+// g + 8n.  BIG: some scale code of the warp is above 128, so that 2^(E - 1) is no bf16 and
+// the factor goes in two steps.
 template <bool BIG>
-__device__ __forceinline__ void kv4_qk(const Kv4Stage& raw, uint8_t* v, const uint32_t (&qa)[9][4],
-                                       int kq, int lane, const uint32_t (&e)[4], float* sp) {
-  const int g = lane >> 2, cq = lane & 3, blk = 4 * kq + cq;
-  // piece i of the block has place (4 blk + i) ^ x: x as in kv4_vplace, the same for g + 8n
-  const uint32_t vb = g * 1024 + 16 * kv4_vplace(4 * blk, g);
-  uint32_t w[4][4], s[4], s2[4];
+__device__ __forceinline__ void kv4_qk(const Kv4Stage& raw, const uint32_t (&qa)[9][4], int kq,
+                                       int lane, const uint32_t (&e)[4], float* sp,
+                                       uint32_t (&v)[4][16]) {
+  const int g = lane >> 2, cq = lane & 3;
   float c[4][4];
+  uint32_t s[4], s2[4];
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    const uint4 u =
-        *reinterpret_cast<const uint4*>(&raw.codes[g + 8 * n][16 * (blk ^ ((g & 1) << 2))]);
-    w[n][0] = u.x;
-    w[n][1] = u.y;
-    w[n][2] = u.z;
-    w[n][3] = u.w;
     s[n] = ((BIG && e[n] > 128u ? 128u : e[n]) + 126u) * 0x00800080u;
     if constexpr (BIG)  // the rest of larger scales: 2^(E - 128), or NaN
       s2[n] = e[n] == 255u ? 0x7FFF7FFFu
                            : ((e[n] > 128u ? e[n] - 128u : 0u) + 127u) * 0x00800080u;
   }
+  auto expand = [&](int n, int i) {
+    e2m1_expand(v[n][4 * i], s[n], &v[n][4 * i]);
+    if constexpr (BIG) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t o[4][4];
+      for (int j = 4 * i; j < 4 * i + 4; ++j) v[n][j] = bf16x2_mul(v[n][j], s2[n]);
+    }
+  };
+  auto product = [&](int n, int k) {  // k: the step of 16 dims
+    if (k == 0)
+      mma_bf16_first(c[n], qa[0], v[n][0], v[n][1]);
+    else
+      mma_bf16(c[n], qa[k], v[n][2 * k], v[n][2 * k + 1]);
+  };
+#pragma unroll
+  for (int n = 0; n < 4; ++n) expand(n, 0);
+  // the products of a word run while the next word's codes are expanded
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      e2m1_expand(w[n][i], s[n], o[n]);
-      if constexpr (BIG) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[n][j] = bf16x2_mul(o[n][j], s2[n]);
-      }
+      if (i < 3) expand(n, i + 1);
+      product((2 * n) & 3, 2 * i + n / 2);
+      product((2 * n + 1) & 3, 2 * i + n / 2);
     }
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      if (i == 0)
-        mma_bf16_first(c[n], qa[0], o[n][0], o[n][1]);
-      else
-        mma_bf16(c[n], qa[2 * i], o[n][0], o[n][1]);
-    }
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      mma_bf16(c[n], qa[2 * i + 1], o[n][2], o[n][3]);
-      *reinterpret_cast<uint4*>(v + ((vb ^ (16u * i)) + 8192u * n)) =
-          make_uint4(o[n][0], o[n][1], o[n][2], o[n][3]);
-    }
-  }
   const uint32_t rope = smem_u32(&raw.rope[(lane & 7) + 8 * (lane >> 4)][0]) + 32 * kq +
                         16 * ((lane >> 3) & 1);
 #pragma unroll
@@ -321,11 +329,12 @@ __device__ __forceinline__ void kv4_qk(const Kv4Stage& raw, uint8_t* v, const ui
   }
 }
 
-// O = alpha O + P V over the expanded tile at v, for dims 128w..128w+127: the same dims
-// that this warp expanded, so only its own lanes' stores are read.
-__device__ __forceinline__ void kv4_pv(uint32_t v, uint32_t pbase, float al0, float al1, int w,
-                                       int lane, float (&o)[16][4]) {
-  // most tiles do not raise any maximum
+// O = alpha O + P V for this warp's dims: a transposed register of v holds, in lane
+// (g', c'), keys 2c', 2c' + 1 of column g' -- just what the MMA takes as its B operand, the
+// columns being the pairs of the four lanes' blocks.
+__device__ __forceinline__ void kv4_pv(const uint32_t (&v)[4][16], uint32_t pbase, float al0,
+                                       float al1, int lane, float (&o)[16][4]) {
+  // most tiles do not move any reference point
   if (!__all_sync(0xffffffffu, al0 == 1.f && al1 == 1.f)) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -336,23 +345,23 @@ __device__ __forceinline__ void kv4_pv(uint32_t v, uint32_t pbase, float al0, fl
     }
   }
   const int pr = (lane & 7) + 8 * ((lane >> 3) & 1);
-  const uint32_t vb = v + pr * 1024 + 16 * kv4_vplace(16 * w + (lane >> 4), pr);
   uint32_t pa[K4_BK / 16][4];
 #pragma unroll
   for (int ks = 0; ks < K4_BK / 16; ++ks)
     ldsm_x4(pbase + (pr * K4_PROW + 16 * ks + 8 * (lane >> 4)) * 2, pa[ks][0], pa[ks][1], pa[ks][2],
             pa[ks][3]);
+  constexpr int kAhead = 3;  // transposes in flight ahead of their product
+  uint32_t t[kAhead][2];
+  auto fetch = [&](int k) {  // k: 16 ks + j
+    t[k % kAhead][0] = transpose8x8(v[2 * (k >> 4)][k & 15]);
+    t[k % kAhead][1] = transpose8x8(v[2 * (k >> 4) + 1][k & 15]);
+  };
 #pragma unroll
-  for (int ks = 0; ks < K4_BK / 16; ++ks) {  // all dims of 16 keys: independent products
+  for (int k = 0; k < kAhead; ++k) fetch(k);
 #pragma unroll
-    for (int np = 0; np < 8; ++np) {
-      // pieces 16w + 2np (+ 1): the second eight lie 128 bytes on, their places turned by 1
-      const uint32_t va = np < 4 ? vb ^ (32u * np) : (vb ^ (32u * (np - 4) + 16u)) + 128u;
-      uint32_t b0, b1, b2, b3;
-      ldsm_x4_t(va + 16384u * ks, b0, b1, b2, b3);
-      mma_bf16(o[2 * np], pa[ks], b0, b1);
-      mma_bf16(o[2 * np + 1], pa[ks], b2, b3);
-    }
+  for (int k = 0; k < 32; ++k) {
+    mma_bf16(o[k & 15], pa[k >> 4], t[k % kAhead][0], t[k % kAhead][1]);
+    if (k + kAhead < 32) fetch(k + kAhead);
   }
 }
 
@@ -368,7 +377,7 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
   const int g = lane >> 2, cq = lane & 3;
   const int sh = 4 * warp + (lane >> 3);  // softmax: head of this lane
   const int sk = 4 * (lane & 7);          // and its four keys
-  const uint32_t vbase = smem_u32(&G.v[0][0]), pbase = smem_u32(&G.p[0][0]);
+  const uint32_t pbase = smem_u32(&G.p[0][0]);
   int stage = grp;
   uint32_t ph = 0;
   const long nj = attn_nitems(a);
@@ -400,22 +409,33 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
     for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m_run = -INFINITY, l_run = 0.f;  // softmax state of head sh (its 8 lanes agree)
 
+    bool ready = false;  // the next tile was seen to have landed
     for (bool last = false; !last;) {
-      if (!mbar_wait(smem_u32(&sm.full[stage]), ph, abort, kErrTimeoutEpilogue)) return;
+      if (!ready && !mbar_wait(smem_u32(&sm.full[stage]), ph, abort, kErrTimeoutEpilogue)) return;
       last = sm.last[stage] != 0;
       const uint32_t vm = sm.vmask[stage];
+      uint32_t v[4][16];
       if (vm) {
         const Kv4Stage& raw = sm.raw[stage];
         uint32_t e[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) e[n] = raw.scale[g + 8 * n][4 * warp + cq];
+        for (int n = 0; n < 4; ++n) {
+          const int blk = 4 * warp + cq;
+          const uint4 u =
+              *reinterpret_cast<const uint4*>(&raw.codes[g + 8 * n][16 * (blk ^ ((g & 1) << 2))]);
+          e[n] = raw.scale[g + 8 * n][blk];
+          v[n][0] = u.x;
+          v[n][4] = u.y;
+          v[n][8] = u.z;
+          v[n][12] = u.w;
+        }
         float* sp = &G.s_part[warp][0][0];
         if (__any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > 128u))
-          kv4_qk<true>(raw, &G.v[0][0], qa, warp, lane, e, sp);
+          kv4_qk<true>(raw, qa, warp, lane, e, sp, v);
         else
-          kv4_qk<false>(raw, &G.v[0][0], qa, warp, lane, e, sp);
+          kv4_qk<false>(raw, qa, warp, lane, e, sp, v);
       }
-      // the partials are complete; the expanded dims stay within the warp that made them
+      // the partials are complete
       named_bar_sync(1 + grp, K4_GTHREADS);
       if (tid == 0) {
         mbar_arrive(smem_u32(&sm.empty[stage]));
@@ -427,6 +447,7 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
         stage = grp;
         ph ^= 1;
       }
+      ready = false;
       if (!vm) continue;
       {
         float4 u = *reinterpret_cast<const float4*>(&G.s_part[0][sh][sk]);
@@ -463,8 +484,10 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
         if ((lane & 7) == 0) G.alpha[sh] = al;
       }
       named_bar_sync(1 + grp, K4_GTHREADS);  // P, alpha complete
-      kv4_pv(vbase, pbase, G.alpha[g], G.alpha[g + 8], warp, lane, o);
-      __syncwarp();
+      // asked before PV, so that the answer's latency hides behind it (an item's first
+      // tile is waited for)
+      if (!last) ready = __all_sync(0xffffffffu, mbar_test(smem_u32(&sm.full[stage]), ph));
+      kv4_pv(v, pbase, G.alpha[g], G.alpha[g + 8], lane, o);
     }
 
     // ---- item epilogue
@@ -475,11 +498,10 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
       G.fin_m[sh] = m_run;
       G.fin_l[sh] = l_run;
     }
-    // this lane holds dims 128 warp + 8j + cq and + cq + 4 of heads g (o[j][0..1]) and g + 8
-    // (o[j][2..3]); group 1 leaves them as four floats per (j, lane)
+    // this lane holds dims 128 warp + 32 cq..+32 of heads g (o[.][0..1]) and g + 8
+    // (o[.][2..3]): dim 8i + j + 4b in o[4i + j][b]; group 1 leaves four floats per (j, lane)
     if (grp == 1) {
-      named_bar_sync(1 + grp, K4_GTHREADS);  // no warp reads its part of the tile any more
-      float4* dst = reinterpret_cast<float4*>(&G.v[0][0]) + warp * 512 + lane;
+      float4* dst = sm.o1 + warp * 512 + lane;
 #pragma unroll
       for (int j = 0; j < 16; ++j) dst[32 * j] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
     }
@@ -500,27 +522,43 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
           wt1[hh] *= inv;
         }
       }
-      const float4* other = reinterpret_cast<const float4*>(&sm.grp[1].v[0][0]) + warp * 512 + lane;
+      const float4* other = sm.o1 + warp * 512 + lane;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float4 u = other[32 * j];
-        const float r[4] = {o[j][0] * wt0[0] + u.x * wt1[0], o[j][1] * wt0[0] + u.y * wt1[0],
-                            o[j][2] * wt0[1] + u.z * wt1[1], o[j][3] * wt0[1] + u.w * wt1[1]};
+        o[j][0] = o[j][0] * wt0[0] + u.x * wt1[0];
+        o[j][1] = o[j][1] * wt0[0] + u.y * wt1[0];
+        o[j][2] = o[j][2] * wt0[1] + u.z * wt1[1];
+        o[j][3] = o[j][3] * wt0[1] + u.w * wt1[1];
+      }
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int h = g + 8 * hh, d = 128 * warp + 8 * j;
-          if (!a.split) {
-            // trade one value with the neighbour: even lanes then hold dims cq, cq + 1, odd
-            // ones cq + 3, cq + 4
-            const float got = __shfl_xor_sync(0xffffffffu, (cq & 1) ? r[2 * hh] : r[2 * hh + 1], 1);
-            *reinterpret_cast<uint32_t*>(a.out + (x.qrow * AT_H + h) * AT_DV + d +
-                                         ((cq & 1) ? cq + 3 : cq)) =
-                (cq & 1) ? pack_bf16(got, r[2 * hh + 1]) : pack_bf16(r[2 * hh], got);
-          } else {
-            float* po = a.part_o + (x.pslot * AT_H + h) * AT_DV + d + cq;
-            po[0] = r[2 * hh];
-            po[4] = r[2 * hh + 1];
+      for (int hh = 0; hh < 2; ++hh) {
+        const int h = g + 8 * hh, d = 128 * warp + 32 * cq;
+        if (!a.split) {
+          uint32_t* ob = reinterpret_cast<uint32_t*>(a.out + (x.qrow * AT_H + h) * AT_DV + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t r[4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              r[2 * b] = pack_bf16(o[4 * i][2 * hh + b], o[4 * i + 1][2 * hh + b]);
+              r[2 * b + 1] = pack_bf16(o[4 * i + 2][2 * hh + b], o[4 * i + 3][2 * hh + b]);
+            }
+            if ((reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
+              reinterpret_cast<uint4*>(ob)[i] = make_uint4(r[0], r[1], r[2], r[3]);
+            } else {  // only required to be aligned to 4
+#pragma unroll
+              for (int b = 0; b < 4; ++b) ob[4 * i + b] = r[b];
+            }
           }
+        } else {
+          float4* po = reinterpret_cast<float4*>(a.part_o + (x.pslot * AT_H + h) * AT_DV + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              po[2 * i + b] = make_float4(o[4 * i][2 * hh + b], o[4 * i + 1][2 * hh + b],
+                                          o[4 * i + 2][2 * hh + b], o[4 * i + 3][2 * hh + b]);
         }
       }
       if (warp == 0 && cq == 0) {
@@ -537,7 +575,7 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
         }
       }
     }
-    named_bar_sync(1 + K4_GROUPS, AT_CONSUMERS);  // group 1's tile and sums have been read
+    named_bar_sync(1 + K4_GROUPS, AT_CONSUMERS);  // group 1's O and sums have been read
   }
 }
 
