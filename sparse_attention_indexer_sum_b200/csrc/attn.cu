@@ -259,8 +259,7 @@ __device__ __forceinline__ long attn_nitems(const AttnArgs& a) {
   const long lo = a.tot * blockIdx.x / gridDim.x, hi = a.tot * (blockIdx.x + 1) / gridDim.x;
   return hi > lo ? (hi - 1) / a.tq - lo / a.tq + 1 : 0;
 }
-// Item j of this CTA (tiles of BK keys).
-template <int BK = AT_BK>
+// Item j of this CTA.
 __device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, long j) {
   AttnItem x;
   if (!a.split) {
@@ -275,8 +274,8 @@ __device__ __forceinline__ AttnItem attn_item(const AttnArgs& a, long j) {
   const long q0 = x.qrow * a.tq;
   const long t0 = lo > q0 ? lo : q0;
   const long t1 = hi < q0 + a.tq ? hi : q0 + a.tq;
-  x.beg = static_cast<int>((t0 - q0) * BK);
-  x.end = min(static_cast<int>((t1 - q0) * BK), a.k);
+  x.beg = static_cast<int>((t0 - q0) * AT_BK);
+  x.end = min(static_cast<int>((t1 - q0) * AT_BK), a.k);
   if (x.end < x.beg) x.end = x.beg;
   x.pslot = x.qrow * a.maxp + (blockIdx.x - attn_cta_of(q0, a.tot, gridDim.x));
   return x;
@@ -341,8 +340,6 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
                                            kErrTimeoutProducer)))
       return false;
     attn_dequant_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
-    if constexpr (FMT == kFmtE4m3 && ADDR == kAddrPaged)
-      attn_zero_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.full[pend_stage]));
     pend_stage = -1;
@@ -804,25 +801,27 @@ __global__ void attn_combine_kernel(const float* part_o, const float* part_ml, i
   o[1] = pack_bf16((a0.z + a1.z) * il, (a0.w + a1.w) * il);
 }
 
-// the kernel of the 4-bit rows (its launch function is used below)
-#include "attn_kv4.cuh"
+// the kernel of the packed rows (its launch function is used below)
+#include "attn_packed.cuh"
 
 // Split plan for few queries: G CTAs over the items*tq (query, tile) pairs, each
 // query cut into at most 64 pieces (G <= 63 * items keeps a range >= tq / 63 tiles).
+// pairs: a CTA takes two tiles at a time, so a range holds at least that many.
 struct SplitPlan {
   bool split;
   int G, tq, maxp;
   long tot;
 };
-static SplitPlan split_plan(long items, int k, int bk = AT_BK) {
+static SplitPlan split_plan(long items, int k, bool pairs = false) {
   SplitPlan p{false, 0, 0, 0, 0};
   const long nsm = num_sms();
   if (items <= 0 || items >= 4 * nsm) return p;  // enough queries for every SM
-  p.tq = (k + bk - 1) / bk;
+  p.tq = (k + AT_BK - 1) / AT_BK;
   p.tot = items * p.tq;
   long G = nsm;
   if (G > p.tot) G = p.tot;
   if (G > 63 * items) G = 63 * items;
+  if (pairs && G > (p.tot + 1) / 2) G = (p.tot + 1) / 2;
   p.G = static_cast<int>(G);
   int mx = 1;
   for (long q = 0; q < items; ++q) {
@@ -836,10 +835,9 @@ static SplitPlan split_plan(long items, int k, int bk = AT_BK) {
 
 size_t attn_mla_ws_bytes(int batch, int rows, int k) {
   const long items = static_cast<long>(batch) * rows;
-  // of either tile size (the 4-bit rows' kernel has tiles of K4_BK keys)
-  const SplitPlan p = split_plan(items, k), p4 = split_plan(items, k, K4_BK);
-  if (!p.split && !p4.split) return 0;
-  const int maxp = p.maxp > p4.maxp ? p.maxp : p4.maxp;
+  const SplitPlan p = split_plan(items, k), pp = split_plan(items, k, true);
+  if (!p.split && !pp.split) return 0;
+  const int maxp = p.maxp > pp.maxp ? p.maxp : pp.maxp;
   return static_cast<size_t>(items) * maxp * AT_H * (AT_DV + 2) * sizeof(float);
 }
 
@@ -864,7 +862,7 @@ ic_status launch_attn_mla(const void* q, const void* kv, long ld_kv, const int* 
   if (nseg < 0 || nseg > IC_MAXSEG || (nseg > 0 && (batch != 1 || !segs)))
     return fail(IC_ERR_INVALID_ARG, "attn: bad segment list (%d)", nseg);
   if (items == 0) return IC_OK;
-  SplitPlan p = split_plan(items, k, fmt == kFmtMxf4 ? K4_BK : AT_BK);
+  SplitPlan p = split_plan(items, k, pages && fmt != kFmtBf16);
   const size_t need = static_cast<size_t>(items) * p.maxp * AT_H * (AT_DV + 2) * sizeof(float);
   // no room, or a workspace the merge's 16-byte loads cannot use: one CTA per query
   if (p.split && (ws == nullptr || need > ws_bytes || reinterpret_cast<uintptr_t>(ws) % 16 != 0))
@@ -892,8 +890,8 @@ ic_status launch_attn_mla(const void* q, const void* kv, long ld_kv, const int* 
   const long grid = p.split ? p.G : (items < num_sms() ? items : num_sms());
   ic_status st;
   if (pages) {
-    st = fmt == kFmtMxf4   ? launch_attn_kv4(a, *pages, grid, stream)
-         : fmt == kFmtE4m3 ? launch_attn_inst<kFmtE4m3, kAddrPaged>(a, *pages, grid, stream)
+    st = fmt == kFmtMxf4   ? launch_attn_packed<kFmtMxf4>(a, *pages, grid, stream)
+         : fmt == kFmtE4m3 ? launch_attn_packed<kFmtE4m3>(a, *pages, grid, stream)
                            : launch_attn_inst<kFmtBf16, kAddrPaged>(a, *pages, grid, stream);
   } else if (nseg > 0) {
     AttnSegs sg;

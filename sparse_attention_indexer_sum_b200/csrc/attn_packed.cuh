@@ -37,52 +37,72 @@
 // barrier that its exchange between warps needed 396 us; sixteen consumer warps (104 registers,
 // spilled) 605 us; PV of a tile and QK of the next in one stretch 457 us.
 
-constexpr int K4_BK = 32;                       // keys per tile
-constexpr int K4_STAGES = 8;                    // a stage always serves one group and one producer
-constexpr int K4_GROUPS = 2;
-constexpr int K4_GTHREADS = AT_CONSUMERS / K4_GROUPS;
-constexpr int K4_PROD_WARPS = 4;
-constexpr int K4_THREADS = AT_CONSUMERS + 32 * K4_PROD_WARPS;
+constexpr int PK_BK = 32;                       // keys per tile
+constexpr int PK_GROUPS = 2;
+constexpr int PK_GTHREADS = AT_CONSUMERS / PK_GROUPS;
+constexpr int PK_PROD_WARPS = 4;
+constexpr int PK_THREADS = AT_CONSUMERS + 32 * PK_PROD_WARPS;
 // Registers per thread after the roles part: the block starts with 168 each (64512 in
-// all), the producers give up theirs above K4_PREGS and the consumers take K4_CREGS.
-constexpr int K4_CREGS = 216, K4_PREGS = 72;
-static_assert(AT_CONSUMERS * K4_CREGS + 32 * K4_PROD_WARPS * K4_PREGS <= 168 * K4_THREADS,
+// all), the producers give up theirs above PK_PREGS and the consumers take PK_CREGS.
+constexpr int PK_CREGS = 216, PK_PREGS = 72;
+static_assert(AT_CONSUMERS * PK_CREGS + 32 * PK_PROD_WARPS * PK_PREGS <= 168 * PK_THREADS,
               "the split must not exceed what the block was launched with");
-static_assert(AT_CONSUMERS % 128 == 0 && K4_PROD_WARPS == 4, "whole warpgroups change registers");
-constexpr int K4_CHUNKS = KV4_ROW_BYTES / 16;   // 16-byte copies per row
-constexpr int K4_SROW = K4_BK + 8;              // padded partial-score row (floats)
-constexpr int K4_PROW = K4_BK + 8;              // padded P row (bf16)
-constexpr int K4_RROW = 144;                    // padded rope row (bytes)
-static_assert(K4_STAGES % K4_GROUPS == 0 && K4_STAGES % K4_PROD_WARPS == 0 &&
-                  K4_PROD_WARPS % K4_GROUPS == 0 && K4_CHUNKS <= 32 && K4_BK == 32,
-              "every use of a stage falls to one group and one producer; a lane per row");
-
-struct Kv4Stage {
-  uint8_t codes[K4_BK][256];  // 16-byte piece i of row r at place i ^ 4 (r & 1)
-  uint8_t rope[K4_BK][K4_RROW];
-  uint8_t scale[K4_BK][16];
+static_assert(AT_CONSUMERS % 128 == 0 && PK_PROD_WARPS == 4, "whole warpgroups change registers");
+constexpr int PK_SROW = PK_BK + 8;              // padded partial-score row (floats)
+constexpr int PK_PROW = PK_BK + 8;              // padded P row (bf16)
+constexpr int PK_RROW = 144;                    // padded rope row (bytes)
+// What differs between the formats.
+template <int FMT>
+struct PackedFmt {
+  static constexpr bool MX = FMT == kFmtMxf4;
+  static constexpr int CODE_ROW = MX ? 256 : 512;      // bytes of a row's codes
+  static constexpr int SWAP = MX ? 4 : 1;              // see PackedStage::codes
+  // a stage always serves one group and one producer
+  static constexpr int STAGES = MX ? 8 : 4;
+  static_assert(STAGES % PK_GROUPS == 0 && STAGES % PK_PROD_WARPS == 0 &&
+                    PK_PROD_WARPS % PK_GROUPS == 0 && PK_BK == 32,
+                "every use of a stage falls to one group and one producer; a lane per row");
+  // The register that holds dim d (0..7) of the eight dims i of a lane's 32, among v[n] or
+  // o, and its half: the pairs are (0, 4), (1, 5), .. as the 4-bit expansion makes them, or
+  // neighbours.
+  static __host__ __device__ constexpr int reg(int i, int d) {
+    return 4 * i + (MX ? (d & 3) : (d >> 1));
+  }
+  static __host__ __device__ constexpr int half(int d) { return MX ? (d >> 2) : (d & 1); }
 };
-struct Kv4Group {  // one consumer group's own
-  alignas(16) float s_part[4][AT_H][K4_SROW];  // partial scores of the dim quarters
-  alignas(16) __nv_bfloat16 p[AT_H][K4_PROW];
+template <int FMT>
+struct PackedStage {
+  // 16-byte piece i of row r at place i ^ SWAP (r & 1): the 16-byte loads of two
+  // neighbouring rows' four lanes then meet no bank twice
+  uint8_t codes[PK_BK][PackedFmt<FMT>::CODE_ROW];
+  uint8_t rope[PK_BK][PK_RROW];
+  uint8_t scale[PK_BK][16];
+};
+struct PackedGroup {  // one consumer group's own
+  alignas(16) float s_part[4][AT_H][PK_SROW];  // partial scores of the dim quarters
+  alignas(16) __nv_bfloat16 p[AT_H][PK_PROW];
   float alpha[AT_H];
   float fin_m[AT_H], fin_l[AT_H];
 };
-struct Kv4Smem {
-  alignas(128) Kv4Stage raw[K4_STAGES];
-  Kv4Group grp[K4_GROUPS];
+template <int FMT>
+struct PackedSmem {
+  static constexpr int STAGES = PackedFmt<FMT>::STAGES;
+  alignas(128) PackedStage<FMT> raw[STAGES];
+  PackedGroup grp[PK_GROUPS];
   alignas(128) uint8_t q[AT_H][AT_ROWB];
   alignas(16) float4 o1[AT_H * AT_DV / 4];  // group 1's O at an item's end
   alignas(16) int ibuf[2][AT_MAXK];
-  uint32_t vmask[K4_STAGES];  // bit j: row j has an entry
-  int last[K4_STAGES];
-  alignas(8) uint64_t full[K4_STAGES];
-  uint64_t empty[K4_STAGES];
+  uint32_t vmask[STAGES];  // bit j: row j has an entry
+  int last[STAGES];
+  alignas(8) uint64_t full[STAGES];
+  uint64_t empty[STAGES];
   uint64_t qfull, qempty;
   uint64_t ifull[2];
   uint64_t pitem;
   int abort;
 };
+static_assert(sizeof(PackedSmem<kFmtMxf4>) <= 232448 && sizeof(PackedSmem<kFmtE4m3>) <= 232448,
+              "shared memory of a CTA");
 
 // 16 bytes to shared memory, or 16 zero bytes if !copy (src is then not read).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool copy) {
@@ -96,36 +116,72 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// The copies of one tile's rows by one warp: prow is lane r's pool row of row r, or -1.
+template <int FMT>
+struct PackedCopy {
+  uint32_t at0, at1, step;  // this lane's piece: its place in even and odd rows, the row step
+  uint32_t at2, step2;      // e4m3: its other piece, of every other row
+  const uint8_t *src, *src2;
+  __device__ __forceinline__ PackedCopy(uint32_t raw0, const void* kv, int lane) {
+    using S = PackedStage<FMT>;
+    const uint8_t* base = static_cast<const uint8_t*>(kv);
+    auto tail = [&](int i, uint32_t& at, uint32_t& st) {  // piece i behind the codes
+      at = raw0 + static_cast<uint32_t>(i == 0 ? offsetof(S, scale) : offsetof(S, rope) + 16 * (i - 1));
+      st = i == 0 ? 16 : PK_RROW;
+    };
+    src = base + 16 * lane;
+    if (FMT == kFmtE4m3 || lane < 16) {
+      at0 = raw0 + static_cast<uint32_t>(offsetof(S, codes)) + 16 * lane;
+      at1 = raw0 + static_cast<uint32_t>(offsetof(S, codes)) + 16 * (lane ^ PackedFmt<FMT>::SWAP);
+      step = PackedFmt<FMT>::CODE_ROW;
+    } else {
+      tail(lane - 16, at0, step);
+      at1 = at0;
+    }
+    if constexpr (FMT == kFmtE4m3) {  // lanes 0..8: even rows, 9..17: odd rows
+      const int i = lane < 9 ? lane : lane < 18 ? lane - 9 : 0;
+      tail(i, at2, step2);
+      if (lane >= 9) at2 += step2;
+      src2 = base + 16 * (32 + i);
+    }
+  }
+  __device__ __forceinline__ void rows(uint32_t stage_ofs, int prow, long ld, int lane) const {
+#pragma unroll
+    for (int r = 0; r < PK_BK; ++r) {
+      const int row = __shfl_sync(0xffffffffu, prow, r);
+      const long ofs = row >= 0 ? static_cast<long>(row) * ld : 0;
+      if (FMT == kFmtE4m3 || lane < 25)
+        cp_async16(((r & 1) ? at1 : at0) + stage_ofs + r * step, src + ofs, row >= 0);
+      if constexpr (FMT == kFmtE4m3) {
+        if (r & 1) {
+          const int row2 = __shfl_sync(0xffffffffu, prow, r - (lane < 9 ? 1 : 0));
+          if (lane < 18)
+            cp_async16(at2 + stage_ofs + (r - 1) * step2,
+                       src2 + (row2 >= 0 ? static_cast<long>(row2) * ld : 0), row2 >= 0);
+        }
+      }
+    }
+  }
+};
+
 // Producers walk the items as attn_producer's do; every fourth tile is one warp's: lane l
-// looks up row l of the tile, then lane l < 25 copies the 16-byte piece l of every row.
-__device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, const PagedArgs& pg) {
+// looks up row l of the tile, then the lanes copy the rows' 16-byte pieces.
+template <int FMT>
+__device__ __forceinline__ void packed_producer(PackedSmem<FMT>& sm, const AttnArgs& a,
+                                                const PagedArgs& pg) {
+  constexpr int STAGES = PackedFmt<FMT>::STAGES;
   const int lane = threadIdx.x & 31;
   const int pw = (threadIdx.x - AT_CONSUMERS) >> 5;
   volatile int* abort = &sm.abort;
   const bool bulk = a.idx_bulk != 0;
-  // this lane's piece: where it lies in a stage for even and odd rows, and the row step
-  uint32_t at0, at1, step;
-  if (lane < 16) {
-    at0 = offsetof(Kv4Stage, codes) + 16 * lane;
-    at1 = offsetof(Kv4Stage, codes) + 16 * (lane ^ 4);
-    step = 256;
-  } else if (lane == 16) {
-    at0 = at1 = offsetof(Kv4Stage, scale);
-    step = 16;
-  } else {
-    at0 = at1 = offsetof(Kv4Stage, rope) + 16 * (lane - 17);
-    step = K4_RROW;
-  }
-  at0 += smem_u32(&sm.raw[0]);
-  at1 += smem_u32(&sm.raw[0]);
-  const uint8_t* src0 = reinterpret_cast<const uint8_t*>(a.kv) + 16 * lane;
+  const PackedCopy<FMT> copy(smem_u32(&sm.raw[0]), a.kv, lane);
   int stage = pw, ib = 0, qloads = 0;
   int t0 = pw;  // this warp's first tile of the item (its tiles of all items: every fourth)
   uint32_t ph = 0, iph[2] = {0u, 0u};
   int ipending[2] = {0, 0};
   const long nj = attn_nitems(a);
   auto load_indices = [&](long it, int b) {
-    const AttnItem x = attn_item<K4_BK>(a, it);
+    const AttnItem x = attn_item(a, it);
     const int cnt = x.end - x.beg;
     const int* src = a.idx + x.qrow * a.k + x.beg;
     if (bulk) {
@@ -142,7 +198,7 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
   };
   if (pw == 0 && nj > 0) load_indices(0, 0);
   for (long it = 0; it < nj; ++it, ib ^= 1) {
-    const AttnItem x = attn_item<K4_BK>(a, it);
+    const AttnItem x = attn_item(a, it);
     const int cnt = x.end - x.beg;
     const long b = x.qrow / a.R;
     const int len = min(pg.seq_lens[b], pg.max_len);
@@ -163,7 +219,7 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
       if (s >= 0 && s < len) lv = j;
     }
     lv = __reduce_max_sync(0xffffffffu, lv);
-    const int ntiles = lv >= 0 ? lv / K4_BK + 1 : 0;
+    const int ntiles = lv >= 0 ? lv / PK_BK + 1 : 0;
     if (pw == 0) {
       // the item's queries, once the consumers hold the previous ones in registers
       if (qloads > 0 &&
@@ -178,7 +234,7 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
     }
     // the pool row of row `lane` of tile t
     auto pool_row = [&](int t) -> int {
-      const int j = t * K4_BK + lane;
+      const int j = t * PK_BK + lane;
       const int s = (t < ntiles && j < cnt) ? ilist[j] : -1;
       if (!in_bounds(s >= -1 && s < len, kErrBoundsGather) || s < 0 || s >= len) return -1;
       return static_cast<int>(attn_page_row(pg, b, s));
@@ -187,39 +243,31 @@ __device__ __forceinline__ void kv4_producer(Kv4Smem& sm, const AttnArgs& a, con
     const int nt = ntiles > 2 ? (ntiles + 1) & ~1 : 2;
     int prow = pool_row(t0);
     bool ok = true;
-    for (int t = t0; t < nt; t += K4_PROD_WARPS) {
-      const int pnext = pool_row(t + K4_PROD_WARPS);
+    for (int t = t0; t < nt; t += PK_PROD_WARPS) {
+      const int pnext = pool_row(t + PK_PROD_WARPS);
       if (!mbar_wait(smem_u32(&sm.empty[stage]), ph ^ 1, abort, kErrTimeoutProducer)) {
         ok = false;
         break;
       }
       const uint32_t valid = __ballot_sync(0xffffffffu, prow >= 0);
-      const uint32_t so = stage * static_cast<uint32_t>(sizeof(Kv4Stage));
-      if (t < ntiles) {  // a tile without entries is not looked at
-#pragma unroll
-        for (int r = 0; r < K4_BK; ++r) {
-          const int row = __shfl_sync(0xffffffffu, prow, r);
-          if (lane < K4_CHUNKS)
-            cp_async16(((r & 1) ? at1 : at0) + so + r * step,
-                       src0 + (row >= 0 ? static_cast<long>(row) * a.ld_kv : 0), row >= 0);
-        }
-      }
+      if (t < ntiles)  // a tile without entries is not looked at
+        copy.rows(stage * static_cast<uint32_t>(sizeof(PackedStage<FMT>)), prow, a.ld_kv, lane);
       const uint32_t fb = smem_u32(&sm.full[stage]);
       cp_async_arrive(fb);
       if (lane == 0) {
         sm.vmask[stage] = valid;
-        sm.last[stage] = t >= nt - K4_GROUPS;
+        sm.last[stage] = t >= nt - PK_GROUPS;
         mbar_arrive(fb);
       }
       prow = pnext;
-      stage += K4_PROD_WARPS;
-      if (stage >= K4_STAGES) {
+      stage += PK_PROD_WARPS;
+      if (stage >= STAGES) {
         stage = pw;
         ph ^= 1;
       }
     }
     // the next item's first tile of this warp: the tiles of all items are dealt in turn
-    t0 = (t0 - nt) & (K4_PROD_WARPS - 1);
+    t0 = (t0 - nt) & (PK_PROD_WARPS - 1);
     if (!ok) break;
   }
   // no copy is in flight when the CTA ends
@@ -250,6 +298,17 @@ __device__ __forceinline__ void e2m1_expand(uint32_t w, uint32_t s, uint32_t* o)
   o[3] = bf16x2_mul(((w8 & 0x00F000F0u) * 0x0104u) & kMask, s);
 }
 
+// Four e4m3 codes times the group's scale, rounded to bf16: the pairs (0, 1), (2, 3).
+__device__ __forceinline__ void e4m3_expand(uint32_t w, float s, uint32_t* o) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(i ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    o[i] = pack_bf16(f.x * s, f.y * s);
+  }
+}
+
 // D = A B (mma_bf16 with nothing to add to).
 __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                                uint32_t b1) {
@@ -267,32 +326,40 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-// Expands the codes of this warp's quarter of a tile into v and multiplies them with Q:
-// dims 128 kq..+128 and rope dims 16 kq..+16 of all keys (lane: keys g + 8n, block
-// 4 kq + cq).  v[n][4i]: the codes of the block's dims 8i..8i+7, which become v[n][4i + j]:
-// dims 8i + j and 8i + j + 4 in bf16.  The partial scores
-// go to sp, the quarter's rows of heads.  e[n]: the scale code of the lane's block of key
-// g + 8n.  BIG: some scale code of the warp is above 128, so that 2^(E - 1) is no bf16 and
-// the factor goes in two steps.
-template <bool BIG>
-__device__ __forceinline__ void kv4_qk(const Kv4Stage& raw, const uint32_t (&qa)[9][4], int kq,
-                                       int lane, const uint32_t (&e)[4], float* sp,
-                                       uint32_t (&v)[4][16]) {
+// Expands the codes of this warp's quarter of a tile in v and multiplies them with Q: dims
+// 128 kq..+128 and rope dims 16 kq..+16 of all keys (lane: keys g + 8n, dims 32 cq..+32 of
+// the quarter).  In v[n][4i] (and v[n][4i + 2] for e4m3) come the codes of dims 8i..8i+7,
+// which become the four pairs v[n][4i..4i+3] (PackedFmt::reg).  The partial scores go to sp,
+// the quarter's rows of heads.  e[n]: key g + 8n's scale: the block's code (4-bit), or the
+// group's fp32 scale as bits.  BIG (4-bit): some scale code of the warp is above 128, so that
+// 2^(E - 1) is no bf16 and the factor goes in two steps.
+template <int FMT, bool BIG>
+__device__ __forceinline__ void packed_qk(const PackedStage<FMT>& raw, const uint32_t (&qa)[9][4],
+                                          int kq, int lane, const uint32_t (&e)[4], float* sp,
+                                          uint32_t (&v)[4][16]) {
   const int g = lane >> 2, cq = lane & 3;
   float c[4][4];
   uint32_t s[4], s2[4];
+  if constexpr (FMT == kFmtMxf4) {
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    s[n] = ((BIG && e[n] > 128u ? 128u : e[n]) + 126u) * 0x00800080u;
-    if constexpr (BIG)  // the rest of larger scales: 2^(E - 128), or NaN
-      s2[n] = e[n] == 255u ? 0x7FFF7FFFu
-                           : ((e[n] > 128u ? e[n] - 128u : 0u) + 127u) * 0x00800080u;
+    for (int n = 0; n < 4; ++n) {
+      s[n] = ((BIG && e[n] > 128u ? 128u : e[n]) + 126u) * 0x00800080u;
+      if constexpr (BIG)  // the rest of larger scales: 2^(E - 128), or NaN
+        s2[n] = e[n] == 255u ? 0x7FFF7FFFu
+                             : ((e[n] > 128u ? e[n] - 128u : 0u) + 127u) * 0x00800080u;
+    }
   }
   auto expand = [&](int n, int i) {
-    e2m1_expand(v[n][4 * i], s[n], &v[n][4 * i]);
-    if constexpr (BIG) {
+    if constexpr (FMT == kFmtE4m3) {
+      const uint32_t w = v[n][4 * i + 2];
+      e4m3_expand(v[n][4 * i], __uint_as_float(e[n]), &v[n][4 * i]);
+      e4m3_expand(w, __uint_as_float(e[n]), &v[n][4 * i + 2]);
+    } else {
+      e2m1_expand(v[n][4 * i], s[n], &v[n][4 * i]);
+      if constexpr (BIG) {
 #pragma unroll
-      for (int j = 4 * i; j < 4 * i + 4; ++j) v[n][j] = bf16x2_mul(v[n][j], s2[n]);
+        for (int j = 4 * i; j < 4 * i + 4; ++j) v[n][j] = bf16x2_mul(v[n][j], s2[n]);
+      }
     }
   };
   auto product = [&](int n, int k) {  // k: the step of 16 dims
@@ -317,22 +384,22 @@ __device__ __forceinline__ void kv4_qk(const Kv4Stage& raw, const uint32_t (&qa)
 #pragma unroll
   for (int n = 0; n < 4; n += 2) {
     uint32_t b0, b1, b2, b3;
-    ldsm_x4(rope + 8 * n * K4_RROW, b0, b1, b2, b3);
+    ldsm_x4(rope + 8 * n * PK_RROW, b0, b1, b2, b3);
     mma_bf16(c[n], qa[8], b0, b1);
     mma_bf16(c[n + 1], qa[8], b2, b3);
   }
   float* p = sp + 2 * cq;
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
-    *reinterpret_cast<float2*>(p + g * K4_SROW + 8 * n) = make_float2(c[n][0], c[n][1]);
-    *reinterpret_cast<float2*>(p + (g + 8) * K4_SROW + 8 * n) = make_float2(c[n][2], c[n][3]);
+    *reinterpret_cast<float2*>(p + g * PK_SROW + 8 * n) = make_float2(c[n][0], c[n][1]);
+    *reinterpret_cast<float2*>(p + (g + 8) * PK_SROW + 8 * n) = make_float2(c[n][2], c[n][3]);
   }
 }
 
 // O = alpha O + P V for this warp's dims: a transposed register of v holds, in lane
 // (g', c'), keys 2c', 2c' + 1 of column g' -- just what the MMA takes as its B operand, the
 // columns being the pairs of the four lanes' blocks.
-__device__ __forceinline__ void kv4_pv(const uint32_t (&v)[4][16], uint32_t pbase, float al0,
+__device__ __forceinline__ void packed_pv(const uint32_t (&v)[4][16], uint32_t pbase, float al0,
                                        float al1, int lane, float (&o)[16][4]) {
   // most tiles do not move any reference point
   if (!__all_sync(0xffffffffu, al0 == 1.f && al1 == 1.f)) {
@@ -345,10 +412,10 @@ __device__ __forceinline__ void kv4_pv(const uint32_t (&v)[4][16], uint32_t pbas
     }
   }
   const int pr = (lane & 7) + 8 * ((lane >> 3) & 1);
-  uint32_t pa[K4_BK / 16][4];
+  uint32_t pa[PK_BK / 16][4];
 #pragma unroll
-  for (int ks = 0; ks < K4_BK / 16; ++ks)
-    ldsm_x4(pbase + (pr * K4_PROW + 16 * ks + 8 * (lane >> 4)) * 2, pa[ks][0], pa[ks][1], pa[ks][2],
+  for (int ks = 0; ks < PK_BK / 16; ++ks)
+    ldsm_x4(pbase + (pr * PK_PROW + 16 * ks + 8 * (lane >> 4)) * 2, pa[ks][0], pa[ks][1], pa[ks][2],
             pa[ks][3]);
   constexpr int kAhead = 3;  // transposes in flight ahead of their product
   uint32_t t[kAhead][2];
@@ -369,10 +436,12 @@ __device__ __forceinline__ void kv4_pv(const uint32_t (&v)[4][16], uint32_t pbas
 // keep their own softmax state and O: while one waits for its softmax or barriers, the
 // other's products run.  At the item's end group 1 leaves its O in shared memory and
 // group 0 merges and stores.
-__device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
-  const int grp = threadIdx.x / K4_GTHREADS, tid = threadIdx.x % K4_GTHREADS;
+template <int FMT>
+__device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnArgs& a) {
+  using F = PackedFmt<FMT>;
+  const int grp = threadIdx.x / PK_GTHREADS, tid = threadIdx.x % PK_GTHREADS;
   const int warp = tid >> 5, lane = tid & 31;
-  Kv4Group& G = sm.grp[grp];
+  PackedGroup& G = sm.grp[grp];
   volatile int* abort = &sm.abort;
   const int g = lane >> 2, cq = lane & 3;
   const int sh = 4 * warp + (lane >> 3);  // softmax: head of this lane
@@ -382,20 +451,27 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
   uint32_t ph = 0;
   const long nj = attn_nitems(a);
   for (long it = 0; it < nj; ++it) {
-    const AttnItem x = attn_item<K4_BK>(a, it);
+    const AttnItem x = attn_item(a, it);
     if (!mbar_wait(smem_u32(&sm.qfull), it & 1, abort, kErrTimeoutEpilogue)) return;
     uint32_t qa[9][4];
-    // dims 128 warp + 32cq + 8i..+8 of heads g, g + 8 in the pairs that e2m1_expand makes
+    // dims 128 warp + 32cq + 8i..+8 of heads g, g + 8 in the pairs of the expanded codes
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int ofs = (128 * warp + 32 * cq + 8 * i) * 2;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const uint4 u = *reinterpret_cast<const uint4*>(&sm.q[g + 8 * hh][ofs]);
-        qa[2 * i][hh] = __byte_perm(u.x, u.z, 0x5410);          // dims 0, 4
-        qa[2 * i][2 + hh] = __byte_perm(u.x, u.z, 0x7632);      // 1, 5
-        qa[2 * i + 1][hh] = __byte_perm(u.y, u.w, 0x5410);      // 2, 6
-        qa[2 * i + 1][2 + hh] = __byte_perm(u.y, u.w, 0x7632);  // 3, 7
+        if constexpr (F::MX) {
+          qa[2 * i][hh] = __byte_perm(u.x, u.z, 0x5410);          // dims 0, 4
+          qa[2 * i][2 + hh] = __byte_perm(u.x, u.z, 0x7632);      // 1, 5
+          qa[2 * i + 1][hh] = __byte_perm(u.y, u.w, 0x5410);      // 2, 6
+          qa[2 * i + 1][2 + hh] = __byte_perm(u.y, u.w, 0x7632);  // 3, 7
+        } else {
+          qa[2 * i][hh] = u.x;
+          qa[2 * i][2 + hh] = u.y;
+          qa[2 * i + 1][hh] = u.z;
+          qa[2 * i + 1][2 + hh] = u.w;
+        }
       }
     }
     ldsm_x4(smem_u32(&sm.q[(lane & 7) + 8 * ((lane >> 3) & 1)][0]) +
@@ -416,34 +492,49 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
       const uint32_t vm = sm.vmask[stage];
       uint32_t v[4][16];
       if (vm) {
-        const Kv4Stage& raw = sm.raw[stage];
+        const PackedStage<FMT>& raw = sm.raw[stage];
         uint32_t e[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const int blk = 4 * warp + cq;
-          const uint4 u =
-              *reinterpret_cast<const uint4*>(&raw.codes[g + 8 * n][16 * (blk ^ ((g & 1) << 2))]);
-          e[n] = raw.scale[g + 8 * n][blk];
-          v[n][0] = u.x;
-          v[n][4] = u.y;
-          v[n][8] = u.z;
-          v[n][12] = u.w;
+          const int r = g + 8 * n, blk = 4 * warp + cq;
+          auto piece = [&](int i) {
+            return *reinterpret_cast<const uint4*>(&raw.codes[r][16 * (i ^ (F::SWAP * (g & 1)))]);
+          };
+          if constexpr (F::MX) {
+            const uint4 u = piece(blk);
+            v[n][0] = u.x;
+            v[n][4] = u.y;
+            v[n][8] = u.z;
+            v[n][12] = u.w;
+            e[n] = raw.scale[r][blk];
+          } else {
+            const uint4 u = piece(2 * blk), w = piece(2 * blk + 1);
+            v[n][0] = u.x;
+            v[n][2] = u.y;
+            v[n][4] = u.z;
+            v[n][6] = u.w;
+            v[n][8] = w.x;
+            v[n][10] = w.y;
+            v[n][12] = w.z;
+            v[n][14] = w.w;
+            e[n] = *reinterpret_cast<const uint32_t*>(&raw.scale[r][4 * warp]);
+          }
         }
         float* sp = &G.s_part[warp][0][0];
-        if (__any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > 128u))
-          kv4_qk<true>(raw, qa, warp, lane, e, sp, v);
+        if (F::MX && __any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > 128u))
+          packed_qk<FMT, F::MX>(raw, qa, warp, lane, e, sp, v);
         else
-          kv4_qk<false>(raw, qa, warp, lane, e, sp, v);
+          packed_qk<FMT, false>(raw, qa, warp, lane, e, sp, v);
       }
       // the partials are complete
-      named_bar_sync(1 + grp, K4_GTHREADS);
+      named_bar_sync(1 + grp, PK_GTHREADS);
       if (tid == 0) {
         mbar_arrive(smem_u32(&sm.empty[stage]));
         if (vm && qheld) mbar_arrive(smem_u32(&sm.qempty));
       }
       if (vm) qheld = false;
-      stage += K4_GROUPS;
-      if (stage >= K4_STAGES) {
+      stage += PK_GROUPS;
+      if (stage >= F::STAGES) {
         stage = grp;
         ph ^= 1;
       }
@@ -483,11 +574,11 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
         *reinterpret_cast<uint2*>(&G.p[sh][sk]) = make_uint2(pack_bf16(e0, e1), pack_bf16(e2, e3));
         if ((lane & 7) == 0) G.alpha[sh] = al;
       }
-      named_bar_sync(1 + grp, K4_GTHREADS);  // P, alpha complete
+      named_bar_sync(1 + grp, PK_GTHREADS);  // P, alpha complete
       // asked before PV, so that the answer's latency hides behind it (an item's first
       // tile is waited for)
       if (!last) ready = __all_sync(0xffffffffu, mbar_test(smem_u32(&sm.full[stage]), ph));
-      kv4_pv(v, pbase, G.alpha[g], G.alpha[g + 8], lane, o);
+      packed_pv(v, pbase, G.alpha[g], G.alpha[g + 8], lane, o);
     }
 
     // ---- item epilogue
@@ -499,13 +590,13 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
       G.fin_l[sh] = l_run;
     }
     // this lane holds dims 128 warp + 32 cq..+32 of heads g (o[.][0..1]) and g + 8
-    // (o[.][2..3]): dim 8i + j + 4b in o[4i + j][b]; group 1 leaves four floats per (j, lane)
+    // (o[.][2..3]), placed as PackedFmt::reg says; group 1 leaves four floats per (j, lane)
     if (grp == 1) {
       float4* dst = sm.o1 + warp * 512 + lane;
 #pragma unroll
       for (int j = 0; j < 16; ++j) dst[32 * j] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
     }
-    named_bar_sync(1 + K4_GROUPS, AT_CONSUMERS);
+    named_bar_sync(1 + PK_GROUPS, AT_CONSUMERS);
     if (grp == 0) {
       float wt0[2], wt1[2], M[2], L[2];  // heads g, g + 8: the groups' weights
 #pragma unroll
@@ -540,10 +631,9 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
           for (int i = 0; i < 4; ++i) {
             uint32_t r[4];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              r[2 * b] = pack_bf16(o[4 * i][2 * hh + b], o[4 * i + 1][2 * hh + b]);
-              r[2 * b + 1] = pack_bf16(o[4 * i + 2][2 * hh + b], o[4 * i + 3][2 * hh + b]);
-            }
+            for (int b = 0; b < 4; ++b)
+              r[b] = pack_bf16(o[F::reg(i, 2 * b)][2 * hh + F::half(2 * b)],
+                               o[F::reg(i, 2 * b + 1)][2 * hh + F::half(2 * b + 1)]);
             if ((reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
               reinterpret_cast<uint4*>(ob)[i] = make_uint4(r[0], r[1], r[2], r[3]);
             } else {  // only required to be aligned to 4
@@ -553,12 +643,13 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
           }
         } else {
           float4* po = reinterpret_cast<float4*>(a.part_o + (x.pslot * AT_H + h) * AT_DV + d);
+          auto at = [&](int i, int b) { return o[F::reg(i, b)][2 * hh + F::half(b)]; };
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
-              po[2 * i + b] = make_float4(o[4 * i][2 * hh + b], o[4 * i + 1][2 * hh + b],
-                                          o[4 * i + 2][2 * hh + b], o[4 * i + 3][2 * hh + b]);
+              po[2 * i + b] = make_float4(at(i, 4 * b), at(i, 4 * b + 1), at(i, 4 * b + 2),
+                                          at(i, 4 * b + 3));
         }
       }
       if (warp == 0 && cq == 0) {
@@ -575,50 +666,52 @@ __device__ __forceinline__ void kv4_consumer(Kv4Smem& sm, const AttnArgs& a) {
         }
       }
     }
-    named_bar_sync(1 + K4_GROUPS, AT_CONSUMERS);  // group 1's O and sums have been read
+    named_bar_sync(1 + PK_GROUPS, AT_CONSUMERS);  // group 1's O and sums have been read
   }
 }
 
-__global__ void __launch_bounds__(K4_THREADS, 1)
-    attn_kv4_kernel(const AttnArgs a, const __grid_constant__ PagedArgs pg) {
+template <int FMT>
+__global__ void __launch_bounds__(PK_THREADS, 1)
+    attn_packed_kernel(const AttnArgs a, const __grid_constant__ PagedArgs pg) {
   // (not rounded up through an integer: the compiler would lose the address space and use
   // generic loads and stores: 434 us instead of 401 on 3 x 341 queries of 2048 rows)
-  extern __shared__ __align__(128) uint8_t kv4_smem[];
-  Kv4Smem& sm = *reinterpret_cast<Kv4Smem*>(kv4_smem);
+  extern __shared__ __align__(128) uint8_t packed_smem[];
+  PackedSmem<FMT>& sm = *reinterpret_cast<PackedSmem<FMT>*>(packed_smem);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < K4_STAGES; ++s) {
+    for (int s = 0; s < PackedFmt<FMT>::STAGES; ++s) {
       // the copies of one producer warp's threads, and its arrival after the flags
       mbar_init(smem_u32(&sm.full[s]), 32 + 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
     mbar_init(smem_u32(&sm.qfull), 1);
-    mbar_init(smem_u32(&sm.qempty), K4_GROUPS);
+    mbar_init(smem_u32(&sm.qempty), PK_GROUPS);
     mbar_init(smem_u32(&sm.ifull[0]), 1);
     mbar_init(smem_u32(&sm.ifull[1]), 1);
-    mbar_init(smem_u32(&sm.pitem), K4_PROD_WARPS);
+    mbar_init(smem_u32(&sm.pitem), PK_PROD_WARPS);
     sm.abort = 0;
     fence_barrier_init();
   }
   __syncthreads();
   grid_dep_wait();  // set-up above touches no global memory
   if (threadIdx.x >= AT_CONSUMERS) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(K4_PREGS));
-    kv4_producer(sm, a, pg);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PK_PREGS));
+    packed_producer(sm, a, pg);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(K4_CREGS));
-    kv4_consumer(sm, a);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PK_CREGS));
+    packed_consumer(sm, a);
   }
   __syncthreads();
 }
 
-static ic_status launch_attn_kv4(const AttnArgs& a, const PagedArgs& pg, long grid,
-                                 cudaStream_t stream) {
-  const int smem = static_cast<int>(sizeof(Kv4Smem));
-  ic_status st = cuda_check(cudaFuncSetAttribute(attn_kv4_kernel,
+template <int FMT>
+static ic_status launch_attn_packed(const AttnArgs& a, const PagedArgs& pg, long grid,
+                                    cudaStream_t stream) {
+  const int smem = static_cast<int>(sizeof(PackedSmem<FMT>));
+  ic_status st = cuda_check(cudaFuncSetAttribute(attn_packed_kernel<FMT>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-                            "cudaFuncSetAttribute(attn_kv4)");
+                            "cudaFuncSetAttribute(attn_packed)");
   if (st) return st;
-  return cuda_check(launch_dep(attn_kv4_kernel, dim3(static_cast<unsigned>(grid)),
-                               dim3(K4_THREADS), smem, stream, 1, a, pg),
-                    "attn_kv4_kernel launch");
+  return cuda_check(launch_dep(attn_packed_kernel<FMT>, dim3(static_cast<unsigned>(grid)),
+                               dim3(PK_THREADS), smem, stream, 1, a, pg),
+                    "attn_packed_kernel launch");
 }

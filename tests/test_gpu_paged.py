@@ -576,7 +576,7 @@ def test_attn_paged_repeated_entries_count_twice_and_bad_pages_are_skipped():
     _check_attn(q, keep, lens, table, page, values, 0.04, out, None)
 
 
-@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", ["bf16"])  # the packed rows have a kernel of their own
 def test_attn_paged_equals_the_contiguous_call(kind):
     g = _gen(15)
     page, n, k = 64, 2048, 500
