@@ -794,8 +794,14 @@ __global__ void attn_combine_kernel(const float* part_o, const float* part_ml, i
 #pragma unroll
   for (int i = 0; i < CMB_PRE; ++i)
     if (i < np) madd((i & 1) ? a1 : a0, wt(i), pv[i]);
-  for (int i = CMB_PRE; i < np; ++i)
-    madd((i & 1) ? a1 : a0, wt(i), *reinterpret_cast<const float4*>(po + i * pstride + d));
+  for (int i0 = CMB_PRE; i0 < np; i0 += CMB_PRE) {  // in batches whose loads overlap
+#pragma unroll
+    for (int i = 0; i < CMB_PRE; ++i)
+      if (i0 + i < np) pv[i] = *reinterpret_cast<const float4*>(po + (i0 + i) * pstride + d);
+#pragma unroll
+    for (int i = 0; i < CMB_PRE; ++i)
+      if (i0 + i < np) madd((i & 1) ? a1 : a0, wt(i0 + i), pv[i]);
+  }
   uint32_t* o = reinterpret_cast<uint32_t*>(out + (qrow * AT_H + h) * AT_DV + d);
   o[0] = pack_bf16((a0.x + a1.x) * il, (a0.y + a1.y) * il);
   o[1] = pack_bf16((a0.z + a1.z) * il, (a0.w + a1.w) * il);

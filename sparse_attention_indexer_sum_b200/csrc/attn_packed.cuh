@@ -99,6 +99,7 @@ struct PackedSmem {
   uint64_t qfull, qempty;
   uint64_t ifull[2];
   uint64_t pitem;
+  uint64_t xfull, xempty;  // an item's O and sums of group 1
   int abort;
 };
 static_assert(sizeof(PackedSmem<kFmtMxf4>) <= 232448 && sizeof(PackedSmem<kFmtE4m3>) <= 232448,
@@ -434,8 +435,8 @@ __device__ __forceinline__ void packed_pv(const uint32_t (&v)[4][16], uint32_t p
 
 // The two groups take the tiles of an item in turn (group j those with index j mod 2) and
 // keep their own softmax state and O: while one waits for its softmax or barriers, the
-// other's products run.  At the item's end group 1 leaves its O in shared memory and
-// group 0 merges and stores.
+// other's products run.  At the item's end group 1 leaves its O in shared memory (and goes
+// on), group 0 merges and stores.
 template <int FMT>
 __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnArgs& a) {
   using F = PackedFmt<FMT>;
@@ -585,6 +586,9 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
     if (qheld && tid == 0) mbar_arrive(smem_u32(&sm.qempty));
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, off);
+    if (grp == 1 && it > 0 &&  // group 0 has read the previous item's
+        !mbar_wait(smem_u32(&sm.xempty), (it - 1) & 1, abort, kErrTimeoutEpilogue))
+      return;
     if ((lane & 7) == 0) {
       G.fin_m[sh] = m_run;
       G.fin_l[sh] = l_run;
@@ -595,9 +599,11 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
       float4* dst = sm.o1 + warp * 512 + lane;
 #pragma unroll
       for (int j = 0; j < 16; ++j) dst[32 * j] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
-    }
-    named_bar_sync(1 + PK_GROUPS, AT_CONSUMERS);
-    if (grp == 0) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.xfull));
+    } else {
+      named_bar_sync(1 + grp, PK_GTHREADS);  // fin_m, fin_l of this group
+      if (!mbar_wait(smem_u32(&sm.xfull), it & 1, abort, kErrTimeoutEpilogue)) return;
       float wt0[2], wt1[2], M[2], L[2];  // heads g, g + 8: the groups' weights
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -665,8 +671,9 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.xempty));  // group 1's O and sums have been read
     }
-    named_bar_sync(1 + PK_GROUPS, AT_CONSUMERS);  // group 1's O and sums have been read
   }
 }
 
@@ -688,6 +695,8 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
     mbar_init(smem_u32(&sm.ifull[0]), 1);
     mbar_init(smem_u32(&sm.ifull[1]), 1);
     mbar_init(smem_u32(&sm.pitem), PK_PROD_WARPS);
+    mbar_init(smem_u32(&sm.xfull), PK_GTHREADS / 32);
+    mbar_init(smem_u32(&sm.xempty), PK_GTHREADS / 32);
     sm.abort = 0;
     fence_barrier_init();
   }
