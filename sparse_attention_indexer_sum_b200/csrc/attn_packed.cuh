@@ -105,7 +105,10 @@ struct PackedSmem {
 static_assert(sizeof(PackedSmem<kFmtMxf4>) <= 232448 && sizeof(PackedSmem<kFmtE4m3>) <= 232448,
               "shared memory of a CTA");
 
-// 16 bytes to shared memory, or 16 zero bytes if !copy (src is then not read).
+// 16 bytes to shared memory; with `copy`, 16 zero bytes if it is false (src is then not read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool copy) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(copy ? 16 : 0)
@@ -121,8 +124,8 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 template <int FMT>
 struct PackedCopy {
   uint32_t at0, at1, step;  // this lane's piece: its place in even and odd rows, the row step
-  uint32_t at2, step2;      // e4m3: its other piece, of every other row
-  const uint8_t *src, *src2;
+  uint32_t at2 = 0, step2 = 0;  // e4m3: its other piece, of every other row
+  const uint8_t *src, *src2 = nullptr;
   __device__ __forceinline__ PackedCopy(uint32_t raw0, const void* kv, int lane) {
     using S = PackedStage<FMT>;
     const uint8_t* base = static_cast<const uint8_t*>(kv);
@@ -147,7 +150,24 @@ struct PackedCopy {
     }
   }
   __device__ __forceinline__ void rows(uint32_t stage_ofs, int prow, long ld, int lane) const {
+    if (__all_sync(0xffffffffu, prow >= 0)) {  // no row is missing: the usual tile
+      uint32_t d0 = at0 + stage_ofs, d1 = at1 + stage_ofs, d2 = at2 + stage_ofs;
 #pragma unroll
+      for (int r = 0; r < PK_BK; r += 2) {
+        const int ra = __shfl_sync(0xffffffffu, prow, r), rb = __shfl_sync(0xffffffffu, prow, r + 1);
+        if (FMT == kFmtE4m3 || lane < 25) {
+          cp_async16(d0, src + static_cast<long>(ra) * ld);
+          cp_async16(d1 + step, src + static_cast<long>(rb) * ld);
+        }
+        if constexpr (FMT == kFmtE4m3)
+          if (lane < 18) cp_async16(d2, src2 + static_cast<long>(lane < 9 ? ra : rb) * ld);
+        d0 += 2 * step;
+        d1 += 2 * step;
+        d2 += 2 * step2;
+      }
+      return;
+    }
+#pragma unroll 4
     for (int r = 0; r < PK_BK; ++r) {
       const int row = __shfl_sync(0xffffffffu, prow, r);
       const long ofs = row >= 0 ? static_cast<long>(row) * ld : 0;

@@ -259,9 +259,9 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s
 // The e8m0 code of a block of magnitude amax >= 0: the smallest power of two 2^(E - 127)
 // with amax / 2^(E - 127) <= 6, so that no value saturates.  amax = m 2^e with m in
 // [1, 2): e - 2 if m <= 1.5, else e - 1; the addition carries into the exponent field
-// exactly when m > 1.5.  (Rounding e down, the other common rule, clips m in (1.5, 2):
-// on normal data its mean squared error is larger.)  A block with an infinity or NaN
-// gets 255 (NaN).
+// exactly when m > 1.5.  (Rounding e down, the other common rule, clips magnitudes with m
+// above 1.5, the block's largest by up to a quarter; its mean squared error is 1 % lower on
+// normal data and 8 % on Laplace data.)  A block with an infinity or NaN gets 255 (NaN).
 __device__ __forceinline__ unsigned e8m0_code(float amax, bool finite) {
   if (!finite) return 255u;
   const int e = static_cast<int>((__float_as_uint(amax) + 0x3FFFFFu) >> 23) - 2;

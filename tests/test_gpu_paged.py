@@ -593,6 +593,92 @@ def test_attn_paged_equals_the_contiguous_call(kind):
     assert torch.equal(dense, got)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "mxf4"])
+def test_attn_paged_loose_alignment_and_wide_tables(kind):
+    """Index lists and outputs at 4-byte addresses, a workspace that the merge cannot use, a
+    cache with longer rows, a block table and lengths inside larger tensors."""
+    g = _gen(21)
+    lens, page, k = [700, 333], 32, 256
+    table, pages = pagedlib.shuffled_table(lens, page, 0, g)
+    cache, values = _latent_pool(pages * page, kind, g)
+    pad = 8 if kind == "bf16" else 16
+    wide = torch.zeros(pages, page, cache.shape[1] + pad, dtype=cache.dtype, device=DEV)
+    wide[..., :cache.shape[1]] = cache.view(pages, page, -1)
+    idx = torch.stack([torch.randperm(n, generator=g)[:k].sort().values for n in lens]).int()
+    flat = torch.empty(2 * k + 1, dtype=torch.int32, device=DEV)
+    loose = flat[1:].view(2, 1, k)
+    loose.copy_(idx[:, None])
+    big = torch.full((2, 40), 1 << 28, dtype=torch.int32, device=DEV)
+    big[:, 3:3 + table.shape[1]] = table.to(DEV)
+    sl = torch.tensor([9] + lens, dtype=torch.int32, device=DEV)[1:]
+    q = torch.randn(2, 1, 16, 576, generator=g).bfloat16().to(DEV)
+    buf = torch.empty(2 * 16 * 512 + 2, dtype=torch.bfloat16, device=DEV)
+    out = buf[2:].view(2, 1, 16, 512)
+    lse = torch.empty(2, 1, 16, device=DEV)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)[4:]
+    for w in (None, ws):
+        out.fill_(0)
+        got = ic.ic_sparse_attn_paged(q, wide[..., :cache.shape[1]], loose,
+                                      big[:, 3:3 + table.shape[1]], sl, 0.04, page_size=page,
+                                      kv_dtype=KINDS[kind], out=out, lse=lse, workspace=w)
+        ic.ic_device_status()
+        assert got is out
+        _check_attn(q, idx[:, None], lens, table, page, values, 0.04, out, lse)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "mxf4"])
+def test_attn_paged_many_empty_and_tiny_queries(kind):
+    """Queries of 0, 1, 31..33 and 64..65 entries one after another in every CTA, with holes
+    that leave a first tile without entries."""
+    g = _gen(22)
+    lens, page, R, k = [128], 16, 1500, 96
+    table, pages = pagedlib.shuffled_table(lens, page, 0, g)
+    cache, values = _latent_pool(pages * page, kind, g)
+    idx = torch.full((1, R, k), -1, dtype=torch.int32)
+    sizes = [0, 1, 31, 32, 33, 64, 65, 96, 0, 0, 5]
+    for r in range(R):
+        m = sizes[r % len(sizes)]
+        idx[0, r, :m] = torch.randperm(128, generator=g)[:m].int()
+        if r % 7 == 3:
+            idx[0, r, :40] = -1
+    q = torch.randn(1, R, 16, 576, generator=g).bfloat16().to(DEV)
+    lse = torch.empty(1, R, 16, device=DEV)
+    out = ic.ic_sparse_attn_paged(q, cache, idx.to(DEV), table.to(DEV),
+                                  torch.tensor(lens, dtype=torch.int32, device=DEV), 0.05,
+                                  page_size=page, kv_dtype=KINDS[kind], lse=lse)
+    ic.ic_device_status()
+    _check_attn(q, idx, lens, table, page, values, 0.05, out, lse)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "mxf4"])
+def test_attn_paged_rising_scores(kind):
+    """Scores that grow along the list, so that the softmax's reference point has to follow,
+    in small steps (within its slack) and in large ones; and falling ones."""
+    g = _gen(23)
+    n, page, k = 512, 64, 512
+    x = torch.zeros(n, 576)
+    x[:, :512] = torch.randn(n, 512, generator=g) * 0.1
+    x[:, 512] = torch.arange(n) / 8.0                    # the score's trend, in a bf16 dim
+    cache = torch.zeros(n, WIDTH[kind], dtype=torch.uint8, device=DEV)
+    ic.ic_cache_append(torch.arange(n, device=DEV), kv=x.bfloat16().to(DEV), kv_cache=cache,
+                       kv_dtype=KINDS[kind])
+    values = pagedlib.unpack(cache, kind)
+    q = torch.randn(1, 4, 16, 576, generator=g)
+    q[..., 512:] = 0
+    for r, slope in enumerate((0.25, 4.0, 200.0, 1000.0)):
+        q[0, r, :, 512] = slope
+    q = q.bfloat16().to(DEV)
+    table = torch.arange(n // page, dtype=torch.int32)[None]
+    sl = torch.tensor([n], dtype=torch.int32, device=DEV)
+    for order in (torch.arange(n), torch.arange(n - 1, -1, -1)):
+        idx = order.int().expand(1, 4, n).contiguous()
+        lse = torch.empty(1, 4, 16, device=DEV)
+        out = ic.ic_sparse_attn_paged(q, cache, idx.to(DEV), table.to(DEV), sl, 0.05,
+                                      page_size=page, kv_dtype=KINDS[kind], lse=lse)
+        ic.ic_device_status()
+        _check_attn(q, idx, [n], table, page, values, 0.05, out, lse)
+
+
 def test_paged_offsets_past_32_bits():
     """Pages at the far end of pools of more than 2^32 bytes."""
     page, n = 64, 300
