@@ -71,19 +71,31 @@ struct E4m3Scale {
     rcp = __frcp_rn(scale);
     divide = !(scale >= 0x1p-90f && scale < INFINITY);
   }
-  __device__ __forceinline__ float quotient(float x) const {
+  __device__ __forceinline__ float fast(float x) const {
     const float q = x * rcp;
-    return divide ? __fdiv_rn(x, scale) : fmaf(fmaf(-q, scale, x), rcp, q);
+    return fmaf(fmaf(-q, scale, x), rcp, q);
   }
   __device__ __forceinline__ uint32_t code(float x) const {
-    return static_cast<uint32_t>(__nv_cvt_float_to_fp8(quotient(x), __NV_SATFINITE, __NV_E4M3));
+    return static_cast<uint32_t>(__nv_cvt_float_to_fp8(divide ? __fdiv_rn(x, scale) : fast(x),
+                                                       __NV_SATFINITE, __NV_E4M3));
   }
-  __device__ __forceinline__ uint32_t code2(float x, float y) const {
-    return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(quotient(x), quotient(y)),
-                                                          __NV_SATFINITE, __NV_E4M3));
+  // The codes of N values (a multiple of 4), four a word.
+  template <int N>
+  __device__ __forceinline__ void codes(const float* v, uint32_t* w) const {
+    if (!divide) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        w[i / 4] = pair(fast(v[i]), fast(v[i + 1])) | (pair(fast(v[i + 2]), fast(v[i + 3])) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        w[i / 4] = pair(__fdiv_rn(v[i], scale), __fdiv_rn(v[i + 1], scale)) |
+                   (pair(__fdiv_rn(v[i + 2], scale), __fdiv_rn(v[i + 3], scale)) << 16);
+    }
   }
-  __device__ __forceinline__ uint32_t code4(const float* v) const {
-    return code2(v[0], v[1]) | (code2(v[2], v[3]) << 16);
+  static __device__ __forceinline__ uint32_t pair(float x, float y) {
+    return static_cast<uint32_t>(
+        __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3));
   }
 };
 
@@ -151,8 +163,9 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const RmsNormArgs a) {
       for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const E4m3Scale sc(amax);
       if (c < chunks) {
-        *reinterpret_cast<uint2*>(a.codes + row * a.ld_c + 8 * c) =
-            make_uint2(sc.code4(&v[i][0]), sc.code4(&v[i][4]));
+        uint32_t w[2];
+        sc.codes<8>(v[i], w);
+        *reinterpret_cast<uint2*>(a.codes + row * a.ld_c + 8 * c) = make_uint2(w[0], w[1]);
         if ((c & 15) == 0) a.scales[row * ((a.n + 127) / 128) + c / 16] = sc.scale;
       }
     }
@@ -273,7 +286,7 @@ __device__ __forceinline__ unsigned e8m0_code(float amax, bool finite) {
 // which the first 64 are rotated.
 // Bound by memory.
 template <int FMT>
-__global__ void __launch_bounds__(128, 12) cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(128, 10) cache_append_kernel(const AppendArgs a) {
   grid_dep_wait();
   const long row = static_cast<long>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
@@ -339,8 +352,9 @@ __global__ void __launch_bounds__(128, 12) cache_append_kernel(const AppendArgs 
         for (int off = 4; off > 0; off >>= 1)  // the 8 lanes of a group of 128
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         const E4m3Scale sc(amax);
-        *reinterpret_cast<uint4*>(o + 16 * lane) =
-            make_uint4(sc.code4(v), sc.code4(v + 4), sc.code4(v + 8), sc.code4(v + 12));
+        uint32_t w[4];
+        sc.codes<16>(v, w);
+        *reinterpret_cast<uint4*>(o + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
         if ((lane & 7) == 0) *reinterpret_cast<float*>(o + 512 + 4 * (lane / 8)) = sc.scale;
         ro = reinterpret_cast<__nv_bfloat16*>(o + 528);
       } else {
@@ -400,7 +414,9 @@ __global__ void __launch_bounds__(128, 12) cache_append_kernel(const AppendArgs 
       for (int off = 16; off > 0; off >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
       const E4m3Scale sc(amax);
-      *reinterpret_cast<uint32_t*>(a.k_cache + slot * 128 + 4 * lane) = sc.code4(v);
+      uint32_t w;
+      sc.codes<4>(v, &w);
+      *reinterpret_cast<uint32_t*>(a.k_cache + slot * 128 + 4 * lane) = w;
       if (lane == 0) a.k_scale[slot] = sc.scale;
     } else {
       uint2 w;
