@@ -1,41 +1,47 @@
-// attn_kv4.cuh -- sparse attention over a paged cache of 4-bit latent rows (included by
+// attn_packed.cuh -- sparse attention over a paged cache of packed latent rows (included by
 // attn.cu, inside its namespace; same items, split and merge as attn_mla_kernel).
 //
-// A row is 400 bytes: 512 e2m1 codes, 16 e8m0 scales (one per 32 dims), 64 bf16 rope
-// dims.  Gathering it moves a third of a bf16 row's bytes, so what bounds this kernel is
-// no longer the gather but turning codes into operands of the warp-level MMA and moving
-// those through shared memory:
-//   * producer warps copy the raw rows with 16-byte cp.async (a row needs 25; a warp takes
-//     a whole tile of 32 rows); rows without an entry become zeros;
+// A row is 400 bytes (512 e2m1 codes, 16 e8m0 scales, one per 32 dims, 64 bf16 rope dims)
+// or 656 (512 e4m3 codes, 4 fp32 scales, one per 128 dims, the same rope dims).  Gathering
+// it moves a third or a half of a bf16 row's bytes, so what bounds this kernel is no longer
+// the gather but turning codes into operands of the warp-level MMA and moving those through
+// shared memory:
+//   * producer warps copy the raw rows with 16-byte cp.async (a row needs 25 or 41; a warp
+//     takes a whole tile of 32 rows); rows without an entry become zeros;
 //   * the eight consumer warps form two groups that take an item's tiles in turn, each with
 //     its own softmax state and O: one group's products fill the other's waits;
 //   * a warp owns 128 latent dims (and 16 rope dims) of its group's tile in QK and in PV.
-//     It expands its codes once, in registers: a lane takes one block, and so one scale, of
-//     four keys with four 16-byte loads (the contraction's order of dims is free, Q's
+//     It expands its codes once, in registers: a lane takes 32 dims, which share one scale,
+//     of four keys with 16-byte loads (the contraction's order of dims is free, Q's
 //     fragments are loaded in the same order).  For PV the expanded registers are turned by
 //     movmatrix into operands with the keys along K: nothing of V goes back to shared
 //     memory;
 //   * the quarters' partial scores meet in shared memory, where the softmax of each head is
 //     computed once.  Its reference point moves only when a score exceeds it by 2^8.
-// Expansion: a code s e e m, its sign at bit 15 and e e m at bits 8..6, is the bf16
+// 4-bit expansion: a code s e e m, its sign at bit 15 and e e m at bits 8..6, is the bf16
 // number value * 2^-126 (0.5 becomes a subnormal); one AND, one multiplication (both
 // shifts at once) and one AND move two codes, and a bf16 multiplication by 2^(E - 1)
-// gives two exact scaled values.
+// gives two exact scaled values.  e4m3 expansion: to fp32, times the scale, rounded to bf16
+// (the one rounding of V and K here; the bf16 operands are what the MMA multiplies).
 //
-// Measured on 3 x 341 queries of 2048 rows of 40000 (2.1 M rows, 7.3e13 flop; L2 holds the
-// cache): 392 us = 187 TFLOP/s, 0.11 of the measured bf16 rate, where the bf16 rows take
-// 400 us in attn_mla_kernel; 64 decode queries over 64 x 200000 rows: 32 us and 6 us for the
-// merge (52 MB of rows, 8 us at the measured HBM rate).  A tile of 32 keys costs an SM 1600
-// cycles; its products alone are 68 x 9 cycles of each tensor pipe (the warp-level MMA at M =
-// 16 heads) and its expansion 600 of each integer pipe, but a warp's chain of load, expand,
-// multiply, exchange, softmax, multiply is 2300 cycles long, and two groups overlap it only in
-// part (registers allow no third: V, O and Q take 164 of a thread's 216).
-// Earlier forms, on the same case: expansion by the producers into bf16 rows for the bf16
+// Measured, 4-bit rows: 3 x 341 queries of 2048 rows of 40000 (2.1 M rows, 7.3e13 flop; L2
+// holds the cache) in 383 us = 191 TFLOP/s, 0.12 of the measured bf16 rate; bf16 rows take
+// 394 us there in attn_mla_kernel, e4m3 rows 477 us.  64 decode queries over 64 x 200000
+// rows, with the merge: 39 us (52 MB of rows, 8 us at the measured HBM rate); bf16 46 us,
+// e4m3 47 us.  A tile of 32 keys costs an SM 1600 cycles; its products alone are 68 x 9
+// cycles of each tensor pipe (the warp-level MMA at M = 16 heads) and its expansion 600 of
+// each integer pipe, but a warp's chain of load, expand, multiply, exchange, softmax,
+// multiply is 2300 cycles long, and two groups overlap it only in part (registers allow no
+// third: V, O and Q take 164 of a thread's 216).
+// Earlier forms, on the first case: expansion by the producers into bf16 rows for the bf16
 // kernel's consumers 875 us; byte-permute tables and a second expansion for PV 561 us (integer
 // pipe); eight warps in step with a swizzled bf16 tile for PV 638 us; that tile with two
-// groups 474 us, with dim quarters 434 us, without generic addresses 401 us, and without the
-// barrier that its exchange between warps needed 396 us; sixteen consumer warps (104 registers,
-// spilled) 605 us; PV of a tile and QK of the next in one stretch 457 us.
+// groups 474 us, with dim quarters 434 us, without generic addresses 401 us, without the
+// barrier that its exchange between warps needed 396 us, with movmatrix instead of the tile
+// 392 us, with mbarriers between the groups 390 us, and with copies that carry no predicate
+// 380 us (383 since all warps leave together after a wait that ran out).  Slower: sixteen
+// consumer warps (104 registers, spilled) 605 us; PV of a tile and QK of the next in one
+// stretch 457 us.
 
 constexpr int PK_BK = 32;                       // keys per tile
 constexpr int PK_GROUPS = 2;
@@ -94,6 +100,7 @@ struct PackedSmem {
   alignas(16) int ibuf[2][AT_MAXK];
   uint32_t vmask[STAGES];  // bit j: row j has an entry
   int last[STAGES];
+  int lost[STAGES];  // the stage's group gives up: a wait ran out
   alignas(8) uint64_t full[STAGES];
   uint64_t empty[STAGES];
   uint64_t qfull, qempty;
@@ -149,8 +156,9 @@ struct PackedCopy {
       src2 = base + 16 * (32 + i);
     }
   }
-  __device__ __forceinline__ void rows(uint32_t stage_ofs, int prow, long ld, int lane) const {
-    if (__all_sync(0xffffffffu, prow >= 0)) {  // no row is missing: the usual tile
+  __device__ __forceinline__ void rows(uint32_t stage_ofs, int prow, uint32_t valid, long ld,
+                                       int lane) const {
+    if (valid == 0xffffffffu) {  // no row is missing: the usual tile
       uint32_t d0 = at0 + stage_ofs, d1 = at1 + stage_ofs, d2 = at2 + stage_ofs;
 #pragma unroll
       for (int r = 0; r < PK_BK; r += 2) {
@@ -217,6 +225,9 @@ __device__ __forceinline__ void packed_producer(PackedSmem<FMT>& sm, const AttnA
       __syncwarp();
     }
   };
+  auto wait = [&](const uint64_t& bar, uint32_t parity) {
+    return mbar_wait(smem_u32(&bar), parity, abort, kErrTimeoutProducer);
+  };
   if (pw == 0 && nj > 0) load_indices(0, 0);
   for (long it = 0; it < nj; ++it, ib ^= 1) {
     const AttnItem x = attn_item(a, it);
@@ -225,27 +236,26 @@ __device__ __forceinline__ void packed_producer(PackedSmem<FMT>& sm, const AttnA
     const int len = min(pg.seq_lens[b], pg.max_len);
     // every producer is done with the previous item (and its index list)
     if (lane == 0) mbar_arrive(smem_u32(&sm.pitem));
-    if (!mbar_wait(smem_u32(&sm.pitem), static_cast<uint32_t>(it & 1), abort, kErrTimeoutProducer))
-      break;
-    if (pw == 0 && it + 1 < nj) load_indices(it + 1, ib ^ 1);
-    if (bulk) {
-      if (!mbar_wait(smem_u32(&sm.ifull[ib]), iph[ib], abort, kErrTimeoutProducer)) break;
-      iph[ib] ^= 1;
-      ipending[ib] = 0;
-    }
+    bool ok = wait(sm.pitem, static_cast<uint32_t>(it & 1));
+    if (bulk) ok = ok && wait(sm.ifull[ib], iph[ib]);
     const int* ilist = sm.ibuf[ib];
     int lv = -1;  // the last entry that counts: later ones need no tiles
     for (int j = lane; j < cnt; j += 32) {
       const int s = ilist[j];
       if (s >= 0 && s < len) lv = j;
     }
-    lv = __reduce_max_sync(0xffffffffu, lv);
+    // after a wait that ran out the warp's lanes leave together, here as below
+    lv = __reduce_max_sync(0xffffffffu, ok ? lv : INT_MAX);
+    if (lv == INT_MAX) break;
+    if (bulk) {
+      iph[ib] ^= 1;
+      ipending[ib] = 0;
+    }
+    if (pw == 0 && it + 1 < nj) load_indices(it + 1, ib ^ 1);
     const int ntiles = lv >= 0 ? lv / PK_BK + 1 : 0;
     if (pw == 0) {
       // the item's queries, once the consumers hold the previous ones in registers
-      if (qloads > 0 &&
-          !mbar_wait(smem_u32(&sm.qempty), (qloads - 1) & 1, abort, kErrTimeoutProducer))
-        break;
+      if (qloads > 0 && !__all_sync(0xffffffffu, wait(sm.qempty, (qloads - 1) & 1))) break;
       if (lane == 0) mbar_arrive_expect_tx(smem_u32(&sm.qfull), AT_H * AT_ROW_BYTES);
       __syncwarp();
       if (lane < AT_H)
@@ -263,16 +273,16 @@ __device__ __forceinline__ void packed_producer(PackedSmem<FMT>& sm, const AttnA
     // the groups take turns: an even number of tiles, at least two
     const int nt = ntiles > 2 ? (ntiles + 1) & ~1 : 2;
     int prow = pool_row(t0);
-    bool ok = true;
     for (int t = t0; t < nt; t += PK_PROD_WARPS) {
       const int pnext = pool_row(t + PK_PROD_WARPS);
-      if (!mbar_wait(smem_u32(&sm.empty[stage]), ph ^ 1, abort, kErrTimeoutProducer)) {
+      const uint32_t valid = __ballot_sync(0xffffffffu, prow >= 0);
+      if (!__all_sync(0xffffffffu, wait(sm.empty[stage], ph ^ 1))) {
         ok = false;
         break;
       }
-      const uint32_t valid = __ballot_sync(0xffffffffu, prow >= 0);
       if (t < ntiles)  // a tile without entries is not looked at
-        copy.rows(stage * static_cast<uint32_t>(sizeof(PackedStage<FMT>)), prow, a.ld_kv, lane);
+        copy.rows(stage * static_cast<uint32_t>(sizeof(PackedStage<FMT>)), prow, valid, a.ld_kv,
+                  lane);
       const uint32_t fb = smem_u32(&sm.full[stage]);
       cp_async_arrive(fb);
       if (lane == 0) {
@@ -470,10 +480,17 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
   const uint32_t pbase = smem_u32(&G.p[0][0]);
   int stage = grp;
   uint32_t ph = 0;
+  // Where a wait ran out (ok is false), the group's warps meet at the first barrier of the
+  // tile at hand, or of the next one, and leave together: none is left in a barrier.
+  bool ok = true;
+  auto wait = [&](const uint64_t& bar, uint32_t parity) {
+    return mbar_wait(smem_u32(&bar), parity, abort, kErrTimeoutEpilogue);
+  };
+  auto lost = [&](int st) { return *const_cast<volatile int*>(&sm.lost[st]) != 0; };
   const long nj = attn_nitems(a);
   for (long it = 0; it < nj; ++it) {
     const AttnItem x = attn_item(a, it);
-    if (!mbar_wait(smem_u32(&sm.qfull), it & 1, abort, kErrTimeoutEpilogue)) return;
+    ok = ok && wait(sm.qfull, it & 1);
     uint32_t qa[9][4];
     // dims 128 warp + 32cq + 8i..+8 of heads g, g + 8 in the pairs of the expanded codes
 #pragma unroll
@@ -508,7 +525,11 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
 
     bool ready = false;  // the next tile was seen to have landed
     for (bool last = false; !last;) {
-      if (!ready && !mbar_wait(smem_u32(&sm.full[stage]), ph, abort, kErrTimeoutEpilogue)) return;
+      if (!__all_sync(0xffffffffu, ok && (ready || wait(sm.full[stage], ph)))) {
+        *const_cast<volatile int*>(&sm.lost[stage]) = 1;
+        named_bar_sync(1 + grp, PK_GTHREADS);
+        return;
+      }
       last = sm.last[stage] != 0;
       const uint32_t vm = sm.vmask[stage];
       uint32_t v[4][16];
@@ -554,13 +575,17 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
         if (vm && qheld) mbar_arrive(smem_u32(&sm.qempty));
       }
       if (vm) qheld = false;
+      const int st = stage;
       stage += PK_GROUPS;
       if (stage >= F::STAGES) {
         stage = grp;
         ph ^= 1;
       }
       ready = false;
-      if (!vm) continue;
+      if (!vm) {
+        if (lost(st)) return;
+        continue;
+      }
       {
         float4 u = *reinterpret_cast<const float4*>(&G.s_part[0][sh][sk]);
 #pragma unroll
@@ -595,10 +620,11 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
         *reinterpret_cast<uint2*>(&G.p[sh][sk]) = make_uint2(pack_bf16(e0, e1), pack_bf16(e2, e3));
         if ((lane & 7) == 0) G.alpha[sh] = al;
       }
+      if (lost(st)) return;
       named_bar_sync(1 + grp, PK_GTHREADS);  // P, alpha complete
       // asked before PV, so that the answer's latency hides behind it (an item's first
       // tile is waited for)
-      if (!last) ready = __all_sync(0xffffffffu, mbar_test(smem_u32(&sm.full[stage]), ph));
+      if (!last) ready = mbar_test(smem_u32(&sm.full[stage]), ph);
       packed_pv(v, pbase, G.alpha[g], G.alpha[g + 8], lane, o);
     }
 
@@ -606,9 +632,7 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
     if (qheld && tid == 0) mbar_arrive(smem_u32(&sm.qempty));
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, off);
-    if (grp == 1 && it > 0 &&  // group 0 has read the previous item's
-        !mbar_wait(smem_u32(&sm.xempty), (it - 1) & 1, abort, kErrTimeoutEpilogue))
-      return;
+    if (grp == 1 && it > 0) ok = wait(sm.xempty, (it - 1) & 1);  // the previous item's is read
     if ((lane & 7) == 0) {
       G.fin_m[sh] = m_run;
       G.fin_l[sh] = l_run;
@@ -623,7 +647,8 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
       if (lane == 0) mbar_arrive(smem_u32(&sm.xfull));
     } else {
       named_bar_sync(1 + grp, PK_GTHREADS);  // fin_m, fin_l of this group
-      if (!mbar_wait(smem_u32(&sm.xfull), it & 1, abort, kErrTimeoutEpilogue)) return;
+      ok = wait(sm.xfull, it & 1);
+      if (!ok) continue;
       float wt0[2], wt1[2], M[2], L[2];  // heads g, g + 8: the groups' weights
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -709,6 +734,7 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
       // the copies of one producer warp's threads, and its arrival after the flags
       mbar_init(smem_u32(&sm.full[s]), 32 + 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
+      sm.lost[s] = 0;
     }
     mbar_init(smem_u32(&sm.qfull), 1);
     mbar_init(smem_u32(&sm.qempty), PK_GROUPS);

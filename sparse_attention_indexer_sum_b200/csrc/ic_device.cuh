@@ -288,11 +288,6 @@ __device__ __forceinline__ uint64_t select_key(float score, uint32_t index) {
   return (static_cast<uint64_t>(score_key(score)) << 32) | static_cast<uint64_t>(~index);
 }
 
-// The power of two that an e8m0 code stands for (2^(code - 127); 255: NaN).
-__device__ __forceinline__ float e8m0_value(unsigned code) {
-  return __uint_as_float(code == 0u ? 0x00400000u : code == 255u ? 0x7FFFFFFFu : code << 23);
-}
-
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
 __device__ __forceinline__ int warp_id() { return __shfl_sync(0xffffffffu, threadIdx.x / 32, 0); }
 
