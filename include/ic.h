@@ -412,7 +412,7 @@ size_t ic_stack_workspace_size(const ic_stack_desc* desc);
  *            ic_quant_e4m3_rows quantises a row, per group of 128 values
  *   scales   [rows, ceil(n / 128)] f32, dense (with codes): the groups' scales
  * At least one of y, codes and h is wanted.  Outputs may be inputs where the list says
- * so, with the same ld; otherwise they must not overlap.  n >= 1; every ld >= n (that
+ * so, with the same ld; otherwise they must not overlap.  1 <= n <= 2^30; every ld >= n (that
  * of an absent matrix is ignored); eps >= 0; |h| < 1.8e19 / sqrt(n), so that the sum of
  * squares stays finite.  Any alignment of the type is taken; rows of a multiple of 8
  * values, up to 16384, at 16-byte aligned addresses (codes: 8) are read only once.
@@ -429,8 +429,8 @@ ic_status ic_rms_norm(const void* x, long ld_x, const void* residual, long ld_r,
  * number * page size + place in the page) or a contiguous one.
  *   slots [rows] int64: token i is written to row slots[i]; a token whose slot is
  *         negative or >= num_slots is not written (a padded batch uses -1).  Slots
- *         of one call are distinct: of two tokens with one slot, every 16 bytes hold
- *         either's.  Other rows are left as they were.
+ *         of one call are distinct: two tokens with one slot leave a mixture of their
+ *         rows there.  Other rows are left as they were.
  *   pos   [rows] int32 positions, rope [rope_rows, 64] f32: row p holds cos(p f_i), i =
  *         0..31, then sin(p f_i).  A token with a position outside [0, rope_rows) is not
  *         written.  rope == NULL: no rotation, pos is ignored.

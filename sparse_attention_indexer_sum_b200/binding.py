@@ -611,6 +611,8 @@ def ic_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, h=None, y=None, 
         if scales.dtype != torch.float32 or not scales.is_contiguous() or \
                 scales.shape != shape[:-1] + (-(-n // 128),):
             raise ValueError("scales must be fp32 [..., %d], contiguous" % -(-n // 128))
+    if rows == 0:
+        return y, codes, scales
     _launch(dev, stream, lambda st: lib().ic_rms_norm(
         x.data_ptr(), ld_x, _ptr(residual), ld_r, _DT[dt], weight.data_ptr(), _DT[weight.dtype],
         eps, rows, n, _ptr(h), ld_h, _ptr(y), ld_y, _ptr(codes), ld_c, _ptr(scales), st))
@@ -777,6 +779,8 @@ def ic_sparse_attn_paged(q, kv_cache, idx, block_table, seq_lens, scale: float, 
         raise ValueError("lse must be fp32 %s" % ((B, R, H),))
     ws, ws_bytes = (None, 0) if workspace is None else (
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if B and R == 0:
+        return out
     _launch(dev, stream, lambda st: lib().ic_sparse_attn_paged(
         q.data_ptr(), kv_cache.data_ptr(), ld, ctypes.byref(pg), idx.data_ptr(), kv_dtype, B, R, H,
         dk, 512, idx.shape[2], scale, out.data_ptr(), _ptr(lse), ws, ws_bytes, st))

@@ -5,6 +5,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <new>
 #include <string>
 #include <vector>
 
@@ -769,7 +770,8 @@ ic_status ic_rms_norm(const void* x, long ld_x, const void* residual, long ld_r,
       (y && ld_y < n) || (codes && ld_codes < n) || !(eps >= 0.f))
     return fail(IC_ERR_INVALID_ARG, "rms_norm: bad sizes (rows %ld n %d, every ld >= n, eps >= 0)",
                 rows, n);
-  if (rows > 0x7fffffffL) return fail(IC_ERR_UNSUPPORTED, "rms_norm: too many rows");
+  if (rows > 0x7fffffffL || n > (1 << 30))
+    return fail(IC_ERR_UNSUPPORTED, "rms_norm: too many rows or values in a row");
   const size_t e = dt == IC_F32 ? 4 : 2;
   if (!aligned(x, e) || !aligned(residual, e) || !aligned(h, e) || !aligned(y, e) ||
       !aligned(weight, w_dt == IC_F32 ? 4 : 2) || !aligned(scales, 4))
@@ -887,8 +889,12 @@ ic_status ic_sparse_attn_paged(const void* q, const void* kv, long ld_kv,
 ic_status ic_decode_step_paged(const char* pattern, const ic_stack_desc* desc,
                                const ic_paging* paging, const ic_layer_io* layers, int nlayers,
                                int* t_cache, void* workspace, size_t ws_bytes, void* stream) {
-  return run_decode_paged(pattern, desc, paging, layers, nlayers, t_cache, workspace, ws_bytes,
-                          static_cast<cudaStream_t>(stream));
+  try {
+    return run_decode_paged(pattern, desc, paging, layers, nlayers, t_cache, workspace, ws_bytes,
+                            static_cast<cudaStream_t>(stream));
+  } catch (const std::bad_alloc&) {  // the list of a pattern's layers
+    return fail(IC_ERR_UNSUPPORTED, "decode_step_paged: no host memory for the layer pattern");
+  }
 }
 
 size_t ic_stack_workspace_size(const ic_stack_desc* d) {

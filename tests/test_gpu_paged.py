@@ -137,6 +137,11 @@ def test_rms_norm_zero_rows_and_non_finite_rows(n):
     assert torch.isnan(y[2]).all() and torch.isnan(y[3, 5])
 
 
+def test_rms_norm_of_no_rows():
+    y, _, _ = ic.ic_rms_norm(torch.empty(0, 64, device=DEV), torch.ones(64, device=DEV))
+    assert y.shape == (0, 64)
+
+
 def test_rms_norm_of_large_values_and_many_rows():
     x = (1e6 * torch.randn(3000, 264, generator=_gen(2))).to(DEV)
     w = torch.randn(264, generator=_gen(3)).to(DEV)
@@ -263,6 +268,29 @@ def test_cache_append_one_of_the_two_caches_and_no_tokens():
     assert torch.equal(kvc[0, slots], kv)
     ic.ic_cache_append(slots[:0], kv=kv[:0], kv_cache=kvc)
     ic.ic_device_status()
+
+
+def test_cache_append_e4m3_equals_the_quantisers_bit_for_bit():
+    """Rows of every magnitude that bf16 has, subnormal ones included, with values down to
+    2^-24 of the largest: the codes and scales of ic_quant_e4m3_rows and ic_pack_kv_e4m3."""
+    g = _gen(21)
+    rows = 262
+    top = torch.arange(-134, 128).double()[:, None]
+    sign = torch.randint(0, 2, (rows, 704), generator=g) * 2 - 1
+    x = sign * (1 + torch.rand(rows, 704, generator=g).double()) * \
+        2.0 ** (top - torch.randint(0, 25, (rows, 704), generator=g))
+    x = x.clamp(-3.3e38, 3.3e38).bfloat16().to(DEV)
+    k, kv = x[:, :128].contiguous(), x[:, 128:].contiguous()
+    kvc = torch.zeros(rows, 656, dtype=torch.uint8, device=DEV)
+    kc = torch.zeros(rows, 128, dtype=torch.uint8, device=DEV)
+    ks = torch.zeros(rows, device=DEV)
+    ic.ic_cache_append(torch.arange(rows, device=DEV), kv=kv, kv_cache=kvc, kv_dtype=ic.IC_E4M3,
+                       k=k, k_cache=kc, k_scale=ks)
+    codes, scales = ic.ic_quant_e4m3_rows(k)
+    packed = ic.ic_pack_kv_e4m3(kv)
+    ic.ic_device_status()
+    assert torch.equal(kc, codes) and torch.equal(ks, scales.flatten())
+    assert torch.equal(kvc, packed.view(rows, 656))
 
 
 def test_cache_append_mxf4_edge_blocks_bit_exact():
@@ -475,6 +503,16 @@ def test_attn_paged(kind, page, R, k, lens):
     _check_attn(q, idx, lens, table, page, values, scale, whole, None)
     again = ic.ic_sparse_attn_paged(*args, workspace=ws, **kw)
     assert torch.equal(out, again)
+
+
+def test_attn_paged_of_no_queries():
+    pool = torch.zeros(4, 16, 576, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(2, 2, dtype=torch.int32, device=DEV)
+    lens = torch.ones(2, dtype=torch.int32, device=DEV)
+    out = ic.ic_sparse_attn_paged(torch.empty(2, 0, 16, 576, dtype=torch.bfloat16, device=DEV), pool,
+                                  torch.empty(2, 0, 8, dtype=torch.int32, device=DEV), table, lens,
+                                  1.0, page_size=16)
+    assert out.shape == (2, 0, 16, 512)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "mxf4"])

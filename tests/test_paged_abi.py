@@ -38,6 +38,7 @@ def _norm(lib, **kw):
     (dict(h=FAKE, ld_h=72), INVALID),                  # h is x with another stride
     (dict(h=ctypes.c_void_p(512), ld_h=64), INVALID),  # h is y
     (dict(rows=1 << 31), UNSUPPORTED),
+    (dict(n=(1 << 30) + 1, ld_x=1 << 31, ld_y=1 << 31), UNSUPPORTED),
 ])
 def test_rms_norm_refusals(lib, kw, want):
     assert _norm(lib, **kw) == want
