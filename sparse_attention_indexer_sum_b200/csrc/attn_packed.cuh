@@ -24,36 +24,42 @@
 // gives two exact scaled values.  e4m3 expansion: to fp32, times the scale, rounded to bf16
 // (the one rounding of V and K here; the bf16 operands are what the MMA multiplies).
 //
-// Measured, 4-bit rows: 3 x 341 queries of 2048 rows of 40000 (2.1 M rows, 7.3e13 flop; L2
-// holds the cache) in 383 us = 191 TFLOP/s, 0.12 of the measured bf16 rate; bf16 rows take
+// Measured, 4-bit rows: 3 x 341 queries of 2048 rows of 40000 (2.1 M rows, 7.3e10 flop; L2
+// holds the cache) in 375 us = 195 TFLOP/s, 0.12 of the measured bf16 rate; bf16 rows take
 // 394 us there in attn_mla_kernel, e4m3 rows 477 us.  64 decode queries over 64 x 200000
 // rows, with the merge: 39 us (52 MB of rows, 8 us at the measured HBM rate); bf16 46 us,
-// e4m3 47 us.  A tile of 32 keys costs an SM 1600 cycles; its products alone are 68 x 9
+// e4m3 47 us.  A tile of 32 keys costs an SM 1550 cycles; its products alone are 68 x 9
 // cycles of each tensor pipe (the warp-level MMA at M = 16 heads) and its expansion 600 of
-// each integer pipe, but a warp's chain of load, expand, multiply, exchange, softmax,
-// multiply is 2300 cycles long, and two groups overlap it only in part (registers allow no
-// third: V, O and Q take 164 of a thread's 216).
+// each integer pipe, but one group's chain is twice that: by the clock, loads, expansion and
+// QK 1300, storing the partials and meeting 300, softmax 360, PV 850 (its 64 transposes keep
+// pace with its 32 products), waits and the item's end 400.  Without the copies it is as
+// long; two groups overlap it only in part, and registers allow no third (V, O and Q take
+// 164 of a thread's 216).
 // Earlier forms, on the first case: expansion by the producers into bf16 rows for the bf16
 // kernel's consumers 875 us; byte-permute tables and a second expansion for PV 561 us (integer
 // pipe); eight warps in step with a swizzled bf16 tile for PV 638 us; that tile with two
 // groups 474 us, with dim quarters 434 us, without generic addresses 401 us, without the
 // barrier that its exchange between warps needed 396 us, with movmatrix instead of the tile
 // 392 us, with mbarriers between the groups 390 us, and with copies that carry no predicate
-// 380 us (383 since all warps leave together after a wait that ran out).  Slower: sixteen
-// consumer warps (104 registers, spilled) 605 us; PV of a tile and QK of the next in one
-// stretch 457 us.
+// 380 us.  Slower: sixteen consumer warps (104 registers, spilled) 605 us; PV of a tile and
+// QK of the next in one stretch 457 us; tiles of 16 keys, in two groups 510 us, in three (of
+// 152 registers a thread) 489 us; the transposes before the softmax or between its steps
+// 410-416 us.
 
 constexpr int PK_BK = 32;                       // keys per tile
+constexpr int PK_NB = PK_BK / 8;                // in blocks of eight
+constexpr int PK_KL = PK_BK / 8;                // softmax: keys of a lane
 constexpr int PK_GROUPS = 2;
-constexpr int PK_GTHREADS = AT_CONSUMERS / PK_GROUPS;
+constexpr int PK_GTHREADS = 128;                // a group: four warps, a quarter of the dims each
+constexpr int PK_CONSUMERS = PK_GROUPS * PK_GTHREADS;
 constexpr int PK_PROD_WARPS = 4;
-constexpr int PK_THREADS = AT_CONSUMERS + 32 * PK_PROD_WARPS;
+constexpr int PK_THREADS = PK_CONSUMERS + 32 * PK_PROD_WARPS;
 // Registers per thread after the roles part: the block starts with 168 each (64512 in
 // all), the producers give up theirs above PK_PREGS and the consumers take PK_CREGS.
 constexpr int PK_CREGS = 216, PK_PREGS = 72;
-static_assert(AT_CONSUMERS * PK_CREGS + 32 * PK_PROD_WARPS * PK_PREGS <= 168 * PK_THREADS,
+static_assert(PK_CONSUMERS * PK_CREGS + 32 * PK_PROD_WARPS * PK_PREGS <= 168 * PK_THREADS,
               "the split must not exceed what the block was launched with");
-static_assert(AT_CONSUMERS % 128 == 0 && PK_PROD_WARPS == 4, "whole warpgroups change registers");
+static_assert(PK_PROD_WARPS == 4 && PK_BK == 32, "whole warpgroups change registers; a lane per row");
 constexpr int PK_SROW = PK_BK + 8;              // padded partial-score row (floats)
 constexpr int PK_PROW = PK_BK + 8;              // padded P row (bf16)
 constexpr int PK_RROW = 144;                    // padded rope row (bytes)
@@ -65,9 +71,8 @@ struct PackedFmt {
   static constexpr int SWAP = MX ? 4 : 1;              // see PackedStage::codes
   // a stage always serves one group and one producer
   static constexpr int STAGES = MX ? 8 : 4;
-  static_assert(STAGES % PK_GROUPS == 0 && STAGES % PK_PROD_WARPS == 0 &&
-                    PK_PROD_WARPS % PK_GROUPS == 0 && PK_BK == 32,
-                "every use of a stage falls to one group and one producer; a lane per row");
+  static_assert(STAGES % PK_GROUPS == 0 && STAGES % PK_PROD_WARPS == 0,
+                "every use of a stage falls to one group and one producer");
   // The register that holds dim d (0..7) of the eight dims i of a lane's 32, among v[n] or
   // o, and its half: the pairs are (0, 4), (1, 5), .. as the 4-bit expansion makes them, or
   // neighbours.
@@ -96,7 +101,7 @@ struct PackedSmem {
   alignas(128) PackedStage<FMT> raw[STAGES];
   PackedGroup grp[PK_GROUPS];
   alignas(128) uint8_t q[AT_H][AT_ROWB];
-  alignas(16) float4 o1[AT_H * AT_DV / 4];  // group 1's O at an item's end
+  alignas(16) float4 o1[PK_GROUPS - 1][AT_H * AT_DV / 4];  // the other groups' O at an item's end
   alignas(16) int ibuf[2][AT_MAXK];
   uint32_t vmask[STAGES];  // bit j: row j has an entry
   int last[STAGES];
@@ -106,7 +111,7 @@ struct PackedSmem {
   uint64_t qfull, qempty;
   uint64_t ifull[2];
   uint64_t pitem;
-  uint64_t xfull, xempty;  // an item's O and sums of group 1
+  uint64_t xfull, xempty;  // an item's O and sums of the groups but the first
   int abort;
 };
 static_assert(sizeof(PackedSmem<kFmtMxf4>) <= 232448 && sizeof(PackedSmem<kFmtE4m3>) <= 232448,
@@ -200,7 +205,7 @@ __device__ __forceinline__ void packed_producer(PackedSmem<FMT>& sm, const AttnA
                                                 const PagedArgs& pg) {
   constexpr int STAGES = PackedFmt<FMT>::STAGES;
   const int lane = threadIdx.x & 31;
-  const int pw = (threadIdx.x - AT_CONSUMERS) >> 5;
+  const int pw = (threadIdx.x - PK_CONSUMERS) >> 5;
   volatile int* abort = &sm.abort;
   const bool bulk = a.idx_bulk != 0;
   const PackedCopy<FMT> copy(smem_u32(&sm.raw[0]), a.kv, lane);
@@ -270,8 +275,8 @@ __device__ __forceinline__ void packed_producer(PackedSmem<FMT>& sm, const AttnA
       if (!in_bounds(s >= -1 && s < len, kErrBoundsGather) || s < 0 || s >= len) return -1;
       return static_cast<int>(attn_page_row(pg, b, s));
     };
-    // the groups take turns: an even number of tiles, at least two
-    const int nt = ntiles > 2 ? (ntiles + 1) & ~1 : 2;
+    // the groups take turns: whole rounds of them, at least one
+    const int nt = max(1, (ntiles + PK_GROUPS - 1) / PK_GROUPS) * PK_GROUPS;
     int prow = pool_row(t0);
     for (int t = t0; t < nt; t += PK_PROD_WARPS) {
       const int pnext = pool_row(t + PK_PROD_WARPS);
@@ -366,14 +371,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // 2^(E - 1) is no bf16 and the factor goes in two steps.
 template <int FMT, bool BIG>
 __device__ __forceinline__ void packed_qk(const PackedStage<FMT>& raw, const uint32_t (&qa)[9][4],
-                                          int kq, int lane, const uint32_t (&e)[4], float* sp,
-                                          uint32_t (&v)[4][16]) {
+                                          int kq, int lane, const uint32_t (&e)[PK_NB], float* sp,
+                                          uint32_t (&v)[PK_NB][16]) {
   const int g = lane >> 2, cq = lane & 3;
-  float c[4][4];
-  uint32_t s[4], s2[4];
+  float c[PK_NB][4];
+  uint32_t s[PK_NB], s2[PK_NB];
   if constexpr (FMT == kFmtMxf4) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < PK_NB; ++n) {
       s[n] = ((BIG && e[n] > 128u ? 128u : e[n]) + 126u) * 0x00800080u;
       if constexpr (BIG)  // the rest of larger scales: 2^(E - 128), or NaN
         s2[n] = e[n] == 255u ? 0x7FFF7FFFu
@@ -394,34 +399,31 @@ __device__ __forceinline__ void packed_qk(const PackedStage<FMT>& raw, const uin
     }
   };
   auto product = [&](int n, int k) {  // k: the step of 16 dims
-    if (k == 0)
-      mma_bf16_first(c[n], qa[0], v[n][0], v[n][1]);
-    else
-      mma_bf16(c[n], qa[k], v[n][2 * k], v[n][2 * k + 1]);
+    mma_bf16(c[n], qa[k], v[n][2 * k], v[n][2 * k + 1]);
   };
+  const uint32_t rope = smem_u32(&raw.rope[(lane & 7) + 8 * (lane >> 4)][0]) + 32 * kq +
+                        16 * ((lane >> 3) & 1);
 #pragma unroll
-  for (int n = 0; n < 4; ++n) expand(n, 0);
+  for (int n = 0; n < PK_NB; n += 2) {
+    uint32_t b0, b1, b2, b3;
+    ldsm_x4(rope + 8 * n * PK_RROW, b0, b1, b2, b3);
+    mma_bf16_first(c[n], qa[8], b0, b1);
+    mma_bf16_first(c[n + 1], qa[8], b2, b3);
+  }
+#pragma unroll
+  for (int n = 0; n < PK_NB; ++n) expand(n, 0);
   // the products of a word run while the next word's codes are expanded
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+    for (int n = 0; n < PK_NB; ++n) {
       if (i < 3) expand(n, i + 1);
-      product((2 * n) & 3, 2 * i + n / 2);
-      product((2 * n + 1) & 3, 2 * i + n / 2);
+      product((2 * n) % PK_NB, 2 * i + 2 * n / PK_NB);
+      product((2 * n + 1) % PK_NB, 2 * i + 2 * n / PK_NB);
     }
-  const uint32_t rope = smem_u32(&raw.rope[(lane & 7) + 8 * (lane >> 4)][0]) + 32 * kq +
-                        16 * ((lane >> 3) & 1);
-#pragma unroll
-  for (int n = 0; n < 4; n += 2) {
-    uint32_t b0, b1, b2, b3;
-    ldsm_x4(rope + 8 * n * PK_RROW, b0, b1, b2, b3);
-    mma_bf16(c[n], qa[8], b0, b1);
-    mma_bf16(c[n + 1], qa[8], b2, b3);
-  }
   float* p = sp + 2 * cq;
 #pragma unroll
-  for (int n = 0; n < 4; ++n) {
+  for (int n = 0; n < PK_NB; ++n) {
     *reinterpret_cast<float2*>(p + g * PK_SROW + 8 * n) = make_float2(c[n][0], c[n][1]);
     *reinterpret_cast<float2*>(p + (g + 8) * PK_SROW + 8 * n) = make_float2(c[n][2], c[n][3]);
   }
@@ -430,7 +432,7 @@ __device__ __forceinline__ void packed_qk(const PackedStage<FMT>& raw, const uin
 // O = alpha O + P V for this warp's dims: a transposed register of v holds, in lane
 // (g', c'), keys 2c', 2c' + 1 of column g' -- just what the MMA takes as its B operand, the
 // columns being the pairs of the four lanes' blocks.
-__device__ __forceinline__ void packed_pv(const uint32_t (&v)[4][16], uint32_t pbase, float al0,
+__device__ __forceinline__ void packed_pv(const uint32_t (&v)[PK_NB][16], uint32_t pbase, float al0,
                                        float al1, int lane, float (&o)[16][4]) {
   // most tiles do not move any reference point
   if (!__all_sync(0xffffffffu, al0 == 1.f && al1 == 1.f)) {
@@ -457,9 +459,9 @@ __device__ __forceinline__ void packed_pv(const uint32_t (&v)[4][16], uint32_t p
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) fetch(k);
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
+  for (int k = 0; k < PK_BK; ++k) {
     mma_bf16(o[k & 15], pa[k >> 4], t[k % kAhead][0], t[k % kAhead][1]);
-    if (k + kAhead < 32) fetch(k + kAhead);
+    if (k + kAhead < PK_BK) fetch(k + kAhead);
   }
 }
 
@@ -476,7 +478,7 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
   volatile int* abort = &sm.abort;
   const int g = lane >> 2, cq = lane & 3;
   const int sh = 4 * warp + (lane >> 3);  // softmax: head of this lane
-  const int sk = 4 * (lane & 7);          // and its four keys
+  const int sk = PK_KL * (lane & 7);      // and its keys
   const uint32_t pbase = smem_u32(&G.p[0][0]);
   int stage = grp;
   uint32_t ph = 0;
@@ -532,12 +534,12 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
       }
       last = sm.last[stage] != 0;
       const uint32_t vm = sm.vmask[stage];
-      uint32_t v[4][16];
+      uint32_t v[PK_NB][16];
       if (vm) {
         const PackedStage<FMT>& raw = sm.raw[stage];
-        uint32_t e[4];
+        uint32_t e[PK_NB];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < PK_NB; ++n) {
           const int r = g + 8 * n, blk = 4 * warp + cq;
           auto piece = [&](int i) {
             return *reinterpret_cast<const uint4*>(&raw.codes[r][16 * (i ^ (F::SWAP * (g & 1)))]);
@@ -563,7 +565,10 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
           }
         }
         float* sp = &G.s_part[warp][0][0];
-        if (F::MX && __any_sync(0xffffffffu, max(max(e[0], e[1]), max(e[2], e[3])) > 128u))
+        uint32_t emax = e[0];
+#pragma unroll
+        for (int n = 1; n < PK_NB; ++n) emax = max(emax, e[n]);
+        if (F::MX && __any_sync(0xffffffffu, emax > 128u))
           packed_qk<FMT, F::MX>(raw, qa, warp, lane, e, sp, v);
         else
           packed_qk<FMT, false>(raw, qa, warp, lane, e, sp, v);
@@ -587,24 +592,25 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
         continue;
       }
       {
-        float4 u = *reinterpret_cast<const float4*>(&G.s_part[0][sh][sk]);
+        float z[PK_KL];
 #pragma unroll
-        for (int qq = 1; qq < 4; ++qq) {
-          const float4 w = *reinterpret_cast<const float4*>(&G.s_part[qq][sh][sk]);
-          u.x += w.x;
-          u.y += w.y;
-          u.z += w.z;
-          u.w += w.w;
+        for (int i = 0; i < PK_KL; i += 2) {
+          float2 u = *reinterpret_cast<const float2*>(&G.s_part[0][sh][sk + i]);
+#pragma unroll
+          for (int qq = 1; qq < 4; ++qq) {
+            const float2 w = *reinterpret_cast<const float2*>(&G.s_part[qq][sh][sk + i]);
+            u.x += w.x;
+            u.y += w.y;
+          }
+          z[i] = ((vm >> (sk + i)) & 1u) ? u.x * a.scale_log2 : -INFINITY;
+          z[i + 1] = ((vm >> (sk + i + 1)) & 1u) ? u.y * a.scale_log2 : -INFINITY;
         }
-        const unsigned vb = vm >> sk;
-        const float z0 = (vb & 1u) ? u.x * a.scale_log2 : -INFINITY;
-        const float z1 = (vb & 2u) ? u.y * a.scale_log2 : -INFINITY;
-        const float z2 = (vb & 4u) ? u.z * a.scale_log2 : -INFINITY;
-        const float z3 = (vb & 8u) ? u.w * a.scale_log2 : -INFINITY;
         // the reference point moves only when a score exceeds it by more than 2^8 in the
         // numerators: their sums have ample room, and most tiles then need no maximum
         // over the head's lanes and no rescaling of O
-        float t = fmaxf(fmaxf(z0, z1), fmaxf(z2, z3)), al = 1.f;
+        float t = z[0], al = 1.f;
+#pragma unroll
+        for (int i = 1; i < PK_KL; ++i) t = fmaxf(t, z[i]);
         if (__any_sync(0xffffffffu, t > m_run + 8.f)) {
 #pragma unroll
           for (int off = 4; off > 0; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
@@ -614,10 +620,12 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
           m_run = n;
         }
         const float bse = (m_run == -INFINITY) ? 0.f : m_run;
-        const float e0 = fast_exp2(z0 - bse), e1 = fast_exp2(z1 - bse);
-        const float e2 = fast_exp2(z2 - bse), e3 = fast_exp2(z3 - bse);
-        l_run += (e0 + e1) + (e2 + e3);  // this lane's four keys' share
-        *reinterpret_cast<uint2*>(&G.p[sh][sk]) = make_uint2(pack_bf16(e0, e1), pack_bf16(e2, e3));
+#pragma unroll
+        for (int i = 0; i < PK_KL; i += 2) {  // this lane's keys' share of the sum
+          const float e0 = fast_exp2(z[i] - bse), e1 = fast_exp2(z[i + 1] - bse);
+          l_run += e0 + e1;
+          *reinterpret_cast<uint32_t*>(&G.p[sh][sk + i]) = pack_bf16(e0, e1);
+        }
         if ((lane & 7) == 0) G.alpha[sh] = al;
       }
       if (lost(st)) return;
@@ -632,15 +640,15 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
     if (qheld && tid == 0) mbar_arrive(smem_u32(&sm.qempty));
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) l_run += __shfl_xor_sync(0xffffffffu, l_run, off);
-    if (grp == 1 && it > 0) ok = wait(sm.xempty, (it - 1) & 1);  // the previous item's is read
+    if (grp > 0 && it > 0) ok = wait(sm.xempty, (it - 1) & 1);  // the previous item's is read
     if ((lane & 7) == 0) {
       G.fin_m[sh] = m_run;
       G.fin_l[sh] = l_run;
     }
     // this lane holds dims 128 warp + 32 cq..+32 of heads g (o[.][0..1]) and g + 8
     // (o[.][2..3]), placed as PackedFmt::reg says; group 1 leaves four floats per (j, lane)
-    if (grp == 1) {
-      float4* dst = sm.o1 + warp * 512 + lane;
+    if (grp > 0) {
+      float4* dst = sm.o1[grp - 1] + warp * 512 + lane;
 #pragma unroll
       for (int j = 0; j < 16; ++j) dst[32 * j] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
       __syncwarp();
@@ -649,29 +657,40 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
       named_bar_sync(1 + grp, PK_GTHREADS);  // fin_m, fin_l of this group
       ok = wait(sm.xfull, it & 1);
       if (!ok) continue;
-      float wt0[2], wt1[2], M[2], L[2];  // heads g, g + 8: the groups' weights
+      float wt[PK_GROUPS][2], M[2], L[2];  // heads g, g + 8: the groups' weights
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int h = g + 8 * hh;
-        const float m0 = G.fin_m[h], m1 = sm.grp[1].fin_m[h];
-        M[hh] = fmaxf(m0, m1);
-        wt0[hh] = m0 == -INFINITY ? 0.f : fast_exp2(m0 - M[hh]);
-        wt1[hh] = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M[hh]);
-        L[hh] = G.fin_l[h] * wt0[hh] + sm.grp[1].fin_l[h] * wt1[hh];
+        M[hh] = sm.grp[0].fin_m[h];
+#pragma unroll
+        for (int x2 = 1; x2 < PK_GROUPS; ++x2) M[hh] = fmaxf(M[hh], sm.grp[x2].fin_m[h]);
+        L[hh] = 0.f;
+#pragma unroll
+        for (int x2 = 0; x2 < PK_GROUPS; ++x2) {
+          const float m = sm.grp[x2].fin_m[h];
+          wt[x2][hh] = m == -INFINITY ? 0.f : fast_exp2(m - M[hh]);
+          L[hh] += sm.grp[x2].fin_l[h] * wt[x2][hh];
+        }
         if (!a.split) {
           const float inv = L[hh] > 0.f ? 1.f / L[hh] : 0.f;
-          wt0[hh] *= inv;
-          wt1[hh] *= inv;
+#pragma unroll
+          for (int x2 = 0; x2 < PK_GROUPS; ++x2) wt[x2][hh] *= inv;
         }
       }
-      const float4* other = sm.o1 + warp * 512 + lane;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float4 u = other[32 * j];
-        o[j][0] = o[j][0] * wt0[0] + u.x * wt1[0];
-        o[j][1] = o[j][1] * wt0[0] + u.y * wt1[0];
-        o[j][2] = o[j][2] * wt0[1] + u.z * wt1[1];
-        o[j][3] = o[j][3] * wt0[1] + u.w * wt1[1];
+        o[j][0] *= wt[0][0];
+        o[j][1] *= wt[0][0];
+        o[j][2] *= wt[0][1];
+        o[j][3] *= wt[0][1];
+#pragma unroll
+        for (int x2 = 1; x2 < PK_GROUPS; ++x2) {
+          const float4 u = sm.o1[x2 - 1][warp * 512 + lane + 32 * j];
+          o[j][0] += u.x * wt[x2][0];
+          o[j][1] += u.y * wt[x2][0];
+          o[j][2] += u.z * wt[x2][1];
+          o[j][3] += u.w * wt[x2][1];
+        }
       }
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -741,14 +760,14 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
     mbar_init(smem_u32(&sm.ifull[0]), 1);
     mbar_init(smem_u32(&sm.ifull[1]), 1);
     mbar_init(smem_u32(&sm.pitem), PK_PROD_WARPS);
-    mbar_init(smem_u32(&sm.xfull), PK_GTHREADS / 32);
+    mbar_init(smem_u32(&sm.xfull), (PK_GROUPS - 1) * PK_GTHREADS / 32);
     mbar_init(smem_u32(&sm.xempty), PK_GTHREADS / 32);
     sm.abort = 0;
     fence_barrier_init();
   }
   __syncthreads();
   grid_dep_wait();  // set-up above touches no global memory
-  if (threadIdx.x >= AT_CONSUMERS) {
+  if (threadIdx.x >= PK_CONSUMERS) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PK_PREGS));
     packed_producer(sm, a, pg);
   } else {
