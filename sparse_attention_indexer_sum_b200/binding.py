@@ -469,19 +469,20 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _one_device(*ts) -> int:
+def _one_device(first, *ts) -> int:
     """The index of the CUDA device that every given tensor lives on (else a ValueError)."""
-    dev = None
+    dev = first.get_device()
     for t in ts:
-        if t is not None:
-            d = t.get_device()
-            if d != dev:
-                if d < 0:
-                    raise ValueError("tensors must be on a CUDA device (got one on %s)" % t.device)
-                if dev is not None:
-                    raise ValueError("tensors are on cuda:%d and cuda:%d" % (dev, d))
-                dev = d
-    return dev
+        if t is not None and t.get_device() != dev:
+            break
+    else:
+        if dev >= 0:
+            return dev
+        t = first
+    bad = [str(u.device) for u in (first, t) if u.get_device() < 0]
+    if bad:
+        raise ValueError("tensors must be on a CUDA device (got one on %s)" % bad[0])
+    raise ValueError("tensors are on cuda:%d and cuda:%d" % (dev, t.get_device()))
 
 
 class _On:
@@ -539,16 +540,21 @@ def _like(t, name, shape, dtype):
     """The row stride of t, which has the given shape."""
     if t.shape != shape:
         raise ValueError("%s must have x's shape" % name)
+    if t.dtype == dtype and t.is_contiguous():
+        return shape[-1]
     return _rows2d(t, name, shape[-1], dtype)[1]
 
 
 def _pool(t, name, dtype, row_bytes=0):
     """(slots, row stride in elements) of a cache [slots, w] or [pages, page_size, w]."""
-    if t.dim() not in (2, 3):
+    shape = t.shape
+    if len(shape) not in (2, 3):
         raise ValueError("%s must be [slots, width] or [pages, page_size, width]" % name)
-    w = t.shape[-1]
+    w = shape[-1]
     if w * t.element_size() < row_bytes:
         raise ValueError("%s rows must hold %d bytes" % (name, row_bytes))
+    if w and t.dtype == dtype and t.is_contiguous():
+        return t.numel() // w, w
     return _rows2d(t, name, w, dtype)
 
 
@@ -562,13 +568,14 @@ def _kv_pool(kv_cache, kv_dtype):
     return kv_dtype, slots, ld
 
 
-def _launch(dev, stream, call):
-    """call(raw stream) with `dev` current; its status is checked."""
-    if stream is None and dev == torch.cuda.current_device():
-        st = call(torch._C._cuda_getCurrentRawStream(dev))  # a tenth of current_stream()'s time
+def _launch(dev, stream, call, *args):
+    """call(*args, raw stream) with `dev` current; its status is checked."""
+    # the raw getters take a tenth of the time of current_device() and current_stream()
+    if stream is None and dev == torch._C._cuda_getDevice():
+        st = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with _On(dev, stream) as raw:
-            st = call(raw)
+            st = call(*args, raw)
     if st != IC_OK:
         raise ICError(st, ic_last_error())
 
@@ -591,7 +598,7 @@ def ic_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, h=None, y=None, 
         raise ValueError("x must be bf16 or fp32 [..., n]")
     n = shape[-1]
     rows, ld_x = _rows2d(x, "x", n, dt)
-    if weight.dtype not in _DT or weight.dim() != 1 or weight.shape[0] != n or \
+    if weight.dtype not in _DT or weight.dim() != 1 or weight.numel() != n or \
             not weight.is_contiguous():
         raise ValueError("weight must be bf16 or fp32 [%d], contiguous" % n)
     dev = _one_device(x, weight, residual, h, y, codes, scales)
@@ -613,9 +620,10 @@ def ic_rms_norm(x, weight, eps: float = 1e-6, *, residual=None, h=None, y=None, 
             raise ValueError("scales must be fp32 [..., %d], contiguous" % -(-n // 128))
     if rows == 0:
         return y, codes, scales
-    _launch(dev, stream, lambda st: lib().ic_rms_norm(
-        x.data_ptr(), ld_x, _ptr(residual), ld_r, _DT[dt], weight.data_ptr(), _DT[weight.dtype],
-        eps, rows, n, _ptr(h), ld_h, _ptr(y), ld_y, _ptr(codes), ld_c, _ptr(scales), st))
+    _launch(dev, stream, lib().ic_rms_norm,
+            x.data_ptr(), ld_x, _ptr(residual), ld_r, _DT[dt], weight.data_ptr(),
+            _DT[weight.dtype], eps, rows, n, _ptr(h), ld_h, _ptr(y), ld_y, _ptr(codes), ld_c,
+            _ptr(scales))
     return y, codes, scales
 
 
@@ -636,7 +644,7 @@ def ic_cache_append(slots, *, kv=None, kv_cache=None, kv_dtype=None, k=None, k_c
     (bf16, or uint8 e4m3 codes with k_scale), rotated by rope [P, 64] at positions pos."""
     if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
         raise ValueError("slots must be int64 [rows], contiguous")
-    rows = slots.shape[0]
+    rows = slots.numel()
     dev = _one_device(slots, kv, kv_cache, k, k_cache, k_scale, pos, rope)
     if (kv is None) != (kv_cache is None) or (k is None) != (k_cache is None):
         raise ValueError("kv goes with kv_cache, k with k_cache")
@@ -649,7 +657,7 @@ def ic_cache_append(slots, *, kv=None, kv_cache=None, kv_dtype=None, k=None, k_c
         if rope.dtype != torch.float32 or rope.dim() != 2 or rope.shape[1] != 64 or \
                 not rope.is_contiguous():
             raise ValueError("rope must be fp32 [positions, 64], contiguous")
-        if pos.dtype != torch.int32 or pos.dim() != 1 or pos.shape[0] != rows or \
+        if pos.dtype != torch.int32 or pos.dim() != 1 or pos.numel() != rows or \
                 not pos.is_contiguous():
             raise ValueError("pos must be int32 [rows], contiguous")
         rope_rows = rope.shape[0]
@@ -670,7 +678,7 @@ def ic_cache_append(slots, *, kv=None, kv_cache=None, kv_dtype=None, k=None, k_c
         elif k_cache.dtype != torch.bfloat16:
             raise ValueError("k_cache must be bf16 or uint8")
         key_slots, ld = _pool(k_cache, "k_cache", k_cache.dtype)
-        if n != rows or ld != 128 or k_cache.shape[-1] != 128:
+        if n != rows or ld != 128 or k_cache.size(-1) != 128:
             raise ValueError("k must have %d rows, k_cache dense rows of 128" % rows)
         if count is not None and key_slots != count:
             raise ValueError("kv_cache and k_cache differ in their number of slots")
@@ -681,10 +689,10 @@ def ic_cache_append(slots, *, kv=None, kv_cache=None, kv_dtype=None, k=None, k_c
     if rows == 0:
         return
     flags = (IC_ROPE_KV_HALVES if kv_halves else 0) | (IC_ROPE_K_HALVES if k_halves else 0)
-    _launch(dev, stream, lambda st: lib().ic_cache_append(
-        rows, slots.data_ptr(), _ptr(pos), _ptr(rope), rope_rows, _ptr(kv), ld_kv, _ptr(kv_cache),
-        ld_cache, kv_dtype, _ptr(k), ld_k, _ptr(k_cache),
-        k_scale.data_ptr() if k_dt == IC_E4M3 else None, k_dt, count, flags, st))
+    _launch(dev, stream, lib().ic_cache_append,
+            rows, slots.data_ptr(), _ptr(pos), _ptr(rope), rope_rows, _ptr(kv), ld_kv,
+            _ptr(kv_cache), ld_cache, kv_dtype, _ptr(k), ld_k, _ptr(k_cache), k_scale.data_ptr() if
+            k_dt == IC_E4M3 else None, k_dt, count, flags)
 
 
 def make_paging(block_table, seq_lens, page_size: int, num_pages: int) -> ic_paging:
@@ -699,7 +707,7 @@ def make_paging(block_table, seq_lens, page_size: int, num_pages: int) -> ic_pag
             raise ValueError("block_table must have contiguous rows")
         if batch > 1:
             ld = block_table.stride(0)
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] != batch or \
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.numel() != batch or \
             not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be int32 [batch], contiguous")
     return ic_paging(block_table.data_ptr(), ld, cols, seq_lens.data_ptr(), page_size, num_pages)
@@ -725,13 +733,14 @@ def ic_indexer_scores_paged(q, k_cache, w, block_table, seq_lens, *, page_size: 
     H, d = q.shape[-2:]
     if d != k_cache.shape[-1] or ld != d:
         raise ValueError("q and k_cache must have dense rows of one length")
-    if q.numel() != B * H * d or w.dtype != torch.float32 or w.numel() != B * H:
+    BH = B * H
+    if q.numel() != BH * d or w.dtype != torch.float32 or w.numel() != BH:
         raise ValueError("q must be [B, H, D] and w fp32 [B, H] with B = %d sequences" % B)
     _contig(q, w)
     fp8 = dt == torch.uint8
     if fp8:
         if q_scale is None or k_scale is None or q_scale.dtype != torch.float32 or \
-                k_scale.dtype != torch.float32 or q_scale.numel() != B * H or \
+                k_scale.dtype != torch.float32 or q_scale.numel() != BH or \
                 k_scale.numel() != slots:
             raise ValueError("e4m3 keys need fp32 q_scale [B, H] and k_scale [slots]")
         _contig(q_scale, k_scale)
@@ -740,19 +749,21 @@ def ic_indexer_scores_paged(q, k_cache, w, block_table, seq_lens, *, page_size: 
     most = cols * page_size
     if scores is None:
         scores = _new((B, most), torch.float32, dev, stream)
-    if scores.dtype != torch.float32 or scores.dim() != 2 or scores.shape[0] != B:
+    if scores.dtype != torch.float32 or scores.dim() != 2:
         raise ValueError("scores must be fp32 [%d, L]" % B)
-    width = scores.shape[1]
+    rows, width = scores.shape
+    if rows != B:
+        raise ValueError("scores must be fp32 [%d, L]" % B)
     ld = width
     if not scores.is_contiguous():
         if width > 1 and scores.stride(1) != 1:
             raise ValueError("scores must have contiguous rows")
         if B > 1:
             ld = scores.stride(0)
-    _launch(dev, stream, lambda st: lib().ic_indexer_scores_paged(
-        q.data_ptr(), q_scale.data_ptr() if fp8 else None, k_cache.data_ptr(),
-        k_scale.data_ptr() if fp8 else None, w.data_ptr(), IC_E4M3 if fp8 else IC_BF16, B, H, d,
-        ctypes.byref(pg), width if width < most else most, scores.data_ptr(), ld, st))
+    _launch(dev, stream, lib().ic_indexer_scores_paged,
+            q.data_ptr(), q_scale.data_ptr() if fp8 else None, k_cache.data_ptr(),
+            k_scale.data_ptr() if fp8 else None, w.data_ptr(), IC_E4M3 if fp8 else IC_BF16, B, H,
+            d, ctypes.byref(pg), width if width < most else most, scores.data_ptr(), ld)
     return scores
 
 
@@ -765,7 +776,8 @@ def ic_sparse_attn_paged(q, kv_cache, idx, block_table, seq_lens, scale: float, 
     if q.dtype != torch.bfloat16 or q.dim() != 4 or idx.dtype != torch.int32 or idx.dim() != 3:
         raise ValueError("q must be bf16 [B, R, H, D] and idx int32 [B, R, k]")
     B, R, H, dk = q.shape
-    if idx.shape[0] != B or idx.shape[1] != R or block_table.shape[0] != B:
+    ib, ir, k = idx.shape
+    if ib != B or ir != R or block_table.shape[0] != B:
         raise ValueError("q, idx and block_table must have one batch and one number of rows")
     _contig(q, idx, out, lse)
     kv_dtype, slots, ld = _kv_pool(kv_cache, kv_dtype)
@@ -781,9 +793,9 @@ def ic_sparse_attn_paged(q, kv_cache, idx, block_table, seq_lens, scale: float, 
         workspace.data_ptr(), workspace.numel() * workspace.element_size())
     if B and R == 0:
         return out
-    _launch(dev, stream, lambda st: lib().ic_sparse_attn_paged(
-        q.data_ptr(), kv_cache.data_ptr(), ld, ctypes.byref(pg), idx.data_ptr(), kv_dtype, B, R, H,
-        dk, 512, idx.shape[2], scale, out.data_ptr(), _ptr(lse), ws, ws_bytes, st))
+    _launch(dev, stream, lib().ic_sparse_attn_paged,
+            q.data_ptr(), kv_cache.data_ptr(), ld, ctypes.byref(pg), idx.data_ptr(), kv_dtype, B,
+            R, H, dk, 512, k, scale, out.data_ptr(), _ptr(lse), ws, ws_bytes)
     return out
 
 
