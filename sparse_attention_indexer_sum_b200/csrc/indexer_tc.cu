@@ -788,8 +788,15 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
         for (int h = 0; h < 64; ++h) wr[t][h] = 0.f;
       uint64_t* stg = reinterpret_cast<uint64_t*>(smem + C::OFF_STG);  // fused: staged keys
       int* scnt = reinterpret_cast<int*>(smem + C::OFF_SCNT);             // and counts
-      for (long i = 0; i < nitems; ++i) {
-        if (C::NSETS > 1 && acc % C::NSETS != set) {  // another set's slot
+      // the set's own tiles: every NSETS'th from its number on (the fused instance's sets
+      // walk all of them, and skip)
+      constexpr int STEP = FUSED ? 1 : C::NSETS;
+      static_assert(C::NACC % STEP == 0, "a set comes back to its own slots");
+      const int skip = STEP > 1 ? set : 0;
+      for (int x = 0; x < skip; ++x) it.advance(a);
+      acc = skip;
+      for (long i = skip; i < nitems; i += STEP) {
+        if (STEP < C::NSETS && acc % C::NSETS != set) {  // another set's slot
           if (++acc == C::NACC) {
             acc = 0;
             aph ^= 1;
@@ -856,10 +863,16 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
 #pragma unroll
           for (int h = 0; h < 64; h += 4) {
             const float4 wv = *reinterpret_cast<const float4*>(wsl + tk * 64 + h);
-            s0 = fmaf(wv.x, fmaxf(v[h + 0], 0.f), s0);
-            s1 = fmaf(wv.y, fmaxf(v[h + 1], 0.f), s1);
-            s2 = fmaf(wv.z, fmaxf(v[h + 2], 0.f), s2);
-            s3 = fmaf(wv.w, fmaxf(v[h + 3], 0.f), s3);
+            const float2 p01 =
+                ffma2(make_float2(wv.x, wv.y),
+                      make_float2(fmaxf(v[h + 0], 0.f), fmaxf(v[h + 1], 0.f)), make_float2(s0, s1));
+            const float2 p23 =
+                ffma2(make_float2(wv.z, wv.w),
+                      make_float2(fmaxf(v[h + 2], 0.f), fmaxf(v[h + 3], 0.f)), make_float2(s2, s3));
+            s0 = p01.x;
+            s1 = p01.y;
+            s2 = p23.x;
+            s3 = p23.y;
           }
           return (s0 + s1) + (s2 + s3);
         };
@@ -984,11 +997,17 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
             }
           }
         }
-        if (++acc == C::NACC) {
-          acc = 0;
+        acc += STEP;
+        if (acc >= C::NACC) {
+          acc -= C::NACC;
           aph ^= 1;
         }
-        it.advance(a);
+        if (STEP > 1 && it.kt + STEP < it.nt) {
+          it.kt += STEP;
+        } else {
+#pragma unroll 1
+          for (int x = 0; x < STEP; ++x) it.advance(a);
+        }
       }
     } else {
       // ------------------------------------------------------------ selectors (fused)
