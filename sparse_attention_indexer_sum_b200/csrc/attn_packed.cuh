@@ -26,7 +26,7 @@
 //
 // Measured, 4-bit rows: 3 x 341 queries of 2048 rows of 40000 (2.1 M rows, 7.3e10 flop; L2
 // holds the cache) in 375 us = 195 TFLOP/s, 0.12 of the measured bf16 rate; bf16 rows take
-// 394 us there in attn_mla_kernel, e4m3 rows 477 us.  64 decode queries over 64 x 200000
+// 394 us there in attn_mla_kernel, e4m3 rows 472 us.  64 decode queries over 64 x 200000
 // rows, with the merge: 39 us (52 MB of rows, 8 us at the measured HBM rate); bf16 46 us,
 // e4m3 47 us.  A tile of 32 keys costs an SM 1550 cycles; its products alone are 68 x 9
 // cycles of each tensor pipe (the warp-level MMA at M = 16 heads) and its expansion 600 of
@@ -73,6 +73,10 @@ struct PackedFmt {
   static constexpr int STAGES = MX ? 8 : 4;
   static_assert(STAGES % PK_GROUPS == 0 && STAGES % PK_PROD_WARPS == 0,
                 "every use of a stage falls to one group and one producer");
+  // pairs of rows that a producer's loop copies in a piece: all 16 of a 4-bit tile (with 4:
+  // 385 instead of 375 us on 3 x 341 queries), 4 of an e4m3 tile, whose rows take more
+  // instructions and spill the producers' registers otherwise (16: 479 instead of 472 us)
+  static constexpr int COPY_PAIRS = MX ? 16 : 4;
   // The register that holds dim d (0..7) of the eight dims i of a lane's 32, among v[n] or
   // o, and its half: the pairs are (0, 4), (1, 5), .. as the 4-bit expansion makes them, or
   // neighbours.
@@ -165,7 +169,8 @@ struct PackedCopy {
                                        int lane) const {
     if (valid == 0xffffffffu) {  // no row is missing: the usual tile
       uint32_t d0 = at0 + stage_ofs, d1 = at1 + stage_ofs, d2 = at2 + stage_ofs;
-#pragma unroll
+      constexpr int kPairs = PackedFmt<FMT>::COPY_PAIRS;
+#pragma unroll kPairs
       for (int r = 0; r < PK_BK; r += 2) {
         const int ra = __shfl_sync(0xffffffffu, prow, r), rb = __shfl_sync(0xffffffffu, prow, r + 1);
         if (FMT == kFmtE4m3 || lane < 25) {
