@@ -489,6 +489,11 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
   uint32_t ph = 0;
   // Where a wait ran out (ok is false), the group's warps meet at the first barrier of the
   // tile at hand, or of the next one, and leave together: none is left in a barrier.
+  // Each lane polls a barrier, the clock and the abort flag by itself, so at the limit some
+  // lanes can have seen the barrier and others not: the warp votes before it branches, and
+  // until then lanes with either answer run the same code.  (A vote, or a __syncwarp, at the
+  // waits for qfull or xempty too, which no branch follows: 385-387 instead of 375 us on
+  // 3 x 341 queries.)
   bool ok = true;
   auto wait = [&](const uint64_t& bar, uint32_t parity) {
     return mbar_wait(smem_u32(&bar), parity, abort, kErrTimeoutEpilogue);
@@ -660,7 +665,7 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
       if (lane == 0) mbar_arrive(smem_u32(&sm.xfull));
     } else {
       named_bar_sync(1 + grp, PK_GTHREADS);  // fin_m, fin_l of this group
-      ok = wait(sm.xfull, it & 1);
+      ok = __all_sync(0xffffffffu, wait(sm.xfull, it & 1));
       if (!ok) continue;
       float wt[PK_GROUPS][2], M[2], L[2];  // heads g, g + 8: the groups' weights
 #pragma unroll
