@@ -488,6 +488,17 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// The reference point of a softmax that was m after scores of at most t.  It stays below
+// infinity, so that a score of +inf leaves inf, not NaN, in the sum.
+__device__ __forceinline__ float softmax_ref(float m, float t) {
+  return fminf(fmaxf(m, t), 3.402823466e38f);
+}
+// The log of the sum (natural) from the sum L of 2^(z_j - M): -inf without entries, NaN where
+// a score is NaN (L is then NaN, and every comparison with it is false).
+__device__ __forceinline__ float attn_lse(float M, float L) {
+  return L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+}
+
 // Partial scores of this warp: Q[:, dims 144kq..+144] . K[keys 16kh..16kh+15] of the
 // tile at kvbase, four accumulator chains (c[0..1]: keys +0..7, c[2..3]: keys +8..15).
 __device__ __forceinline__ void attn_qk(uint32_t kvbase, const uint32_t (&qa)[9][4], int kq,
@@ -630,7 +641,7 @@ __device__ __forceinline__ void attn_consumer(AttnSmem& sm, const AttnArgs& a) {
         float t = fmaxf(z0, z1);
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-        const float n = fmaxf(m_run, t);
+        const float n = softmax_ref(m_run, t);
         const float al = (n == -INFINITY) ? 1.f : fast_exp2(m_run - n);
         const float bse = (n == -INFINITY) ? 0.f : n;
         const float e0 = fast_exp2(z0 - bse), e1 = fast_exp2(z1 - bse);
@@ -673,9 +684,8 @@ __device__ __forceinline__ void attn_consumer(AttnSmem& sm, const AttnArgs& a) {
             pack_bf16(o[i][2] * inv1, o[i][3] * inv1);
       }
       if (a.lse && warp == 0 && cq == 0) {
-        a.lse[x.qrow * AT_H + g] = L0 > 0.f ? (M0 + log2f(L0)) * 0.69314718055994531f : -INFINITY;
-        a.lse[x.qrow * AT_H + g + 8] =
-            L1 > 0.f ? (M1 + log2f(L1)) * 0.69314718055994531f : -INFINITY;
+        a.lse[x.qrow * AT_H + g] = attn_lse(M0, L0);
+        a.lse[x.qrow * AT_H + g + 8] = attn_lse(M1, L1);
       }
     } else {
       const long ps = x.pslot;
@@ -779,7 +789,7 @@ __global__ void attn_combine_kernel(const float* part_o, const float* part_ml, i
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     il = L > 0.f ? 1.f / L : 0.f;
     if (threadIdx.x == 0 && lse)
-      lse[qrow * AT_H + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+      lse[qrow * AT_H + h] = attn_lse(M, L);
   }
   // weight of piece i (held by lane i % 32)
   auto wt = [&](int i) { return __shfl_sync(0xffffffffu, i < 32 ? w0 : w1, i & 31); };
@@ -989,11 +999,12 @@ __global__ void attn_f32_kernel(const float* q, const float* kv, long ld_kv, con
     if ((tid & 31) == 0) red[tid >> 5] = lmax;
     __syncthreads();
     float M = -INFINITY;
-    for (int i = 0; i < (nt + 31) / 32; ++i) M = fmaxf(M, red[i]);
+    for (int i = 0; i < (nt + 31) / 32; ++i) M = softmax_ref(M, red[i]);
     __syncthreads();
     float lsum = 0.f;
     for (int j = tid; j < k; j += nt) {
-      const float e = (M == -INFINITY) ? 0.f : expf(z[j] - M);
+      // (M is -inf if no score is a number above it: skipped entries then give 0, NaN stays)
+      const float e = expf(z[j] - (M == -INFINITY ? 0.f : M));
       z[j] = e;
       lsum += e;
     }
@@ -1011,7 +1022,7 @@ __global__ void attn_f32_kernel(const float* q, const float* kv, long ld_kv, con
       }
       out[(qrow * heads + h) * dv + d] = acc * inv;
     }
-    if (lse && tid == 0) lse[qrow * heads + h] = L > 0.f ? M + logf(L) : -INFINITY;
+    if (lse && tid == 0) lse[qrow * heads + h] = L == 0.f ? -INFINITY : M + logf(L);
     __syncthreads();
   }
 }

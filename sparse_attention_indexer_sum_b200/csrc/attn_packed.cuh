@@ -624,7 +624,7 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
         if (__any_sync(0xffffffffu, t > m_run + 8.f)) {
 #pragma unroll
           for (int off = 4; off > 0; off >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-          const float n = fmaxf(m_run, t);
+          const float n = softmax_ref(m_run, t);
           al = (n == -INFINITY) ? 1.f : fast_exp2(m_run - n);
           l_run *= al;
           m_run = n;
@@ -740,8 +740,7 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
             a.part_ml[(x.pslot * AT_H + h) * 2] = M[hh];
             a.part_ml[(x.pslot * AT_H + h) * 2 + 1] = L[hh];
           } else if (a.lse) {
-            a.lse[x.qrow * AT_H + h] =
-                L[hh] > 0.f ? (M[hh] + log2f(L[hh])) * 0.69314718055994531f : -INFINITY;
+            a.lse[x.qrow * AT_H + h] = attn_lse(M[hh], L[hh]);
           }
         }
       }
