@@ -141,31 +141,21 @@ __device__ __forceinline__ void attn_kv_range(const AttnArgs& a, const AttnAddrP
   }
 }
 
-// Paged instances: zeros the rows of one tile stage of producer warp pw that receive
-// no copy, so that a NaN or infinity left there by an earlier query's row cannot
-// reach this one through 0 * NaN.  Only tiles with missing rows have any.
-__device__ __forceinline__ void attn_zero_rows(uint8_t* stage_rows, unsigned valid, int pw) {
-  unsigned miss = ~valid & (0xFFu << (8 * pw));
-  if (!miss) return;
-  for (; miss; miss &= miss - 1) {
-    uint4* row = reinterpret_cast<uint4*>(stage_rows + (__ffs(miss) - 1) * AT_ROWB);
-    for (int i = threadIdx.x & 31; i < AT_DK * 2 / 16; i += 32) row[i] = make_uint4(0, 0, 0, 0);
-  }
-  fence_proxy_async_smem();  // before a later copy lands where these stores went
-}
+// A tile's rows without an entry are copied from here (row j of a tile from row j, so that
+// the CTAs' reads spread), so that a NaN or infinity which an earlier query's row left in the
+// stage cannot reach this one through 0 * NaN.  Never written.
+static __device__ __align__(128) const uint8_t g_zero_rows[AT_BK][AT_ROW_BYTES] = {};
 
 // Dequantises the fp8 rows of one tile stage that belong to producer warp pw (rows
-// 8pw..8pw+7 with their bit set in `valid`) in place: a raw row (656 bytes at slot
+// 8pw..8pw+7) in place: a raw row (656 bytes at slot
 // offset 512) becomes the 576 bf16 values of the row at offset 0, latent code *
 // its group's scale rounded to bf16, rope copied.  Lane l owns latent dims
 // 16l..16l+15 of every row (and rope bytes 16l..16l+15 for l < 8).  All eight
 // rows are loaded before any store, so the overlapping expansion is safe and the
-// rows' loads overlap; rows without a copy are left as they are (finite values
-// of an earlier tile).
-__device__ __forceinline__ void attn_dequant_rows(uint8_t* stage_rows, unsigned valid, int pw) {
+// rows' loads overlap.
+__device__ __forceinline__ void attn_dequant_rows(uint8_t* stage_rows, int pw) {
   const int lane = threadIdx.x & 31;
   uint8_t* rows = stage_rows + 8 * pw * AT_ROWB;
-  const unsigned mine = (valid >> (8 * pw)) & 0xFFu;
   uint4 codes[8], rope[8];
   float sc[8];
 #pragma unroll
@@ -179,7 +169,6 @@ __device__ __forceinline__ void attn_dequant_rows(uint8_t* stage_rows, unsigned 
   __syncwarp();
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    if (!((mine >> r) & 1u)) continue;
     uint8_t* row = rows + r * AT_ROWB;
     const __nv_fp8x2_storage_t* cp = reinterpret_cast<const __nv_fp8x2_storage_t*>(&codes[r]);
     uint32_t o[8];
@@ -326,20 +315,20 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
   int ipending[2] = {0, 0};
   const uint32_t kv0 = smem_u32(&sm.kv[0][0][0]);
   const bool mine = (lane >> 3) == pw;  // this lane issues its row's copy
+  const void* zeros = g_zero_rows[lane];
   int ib = 0;
   long nitem = 0;
   const long nj = attn_nitems(a);
-  // fp8 cache: the stage, phase and valid rows of the tile whose raw rows are the
-  // next to dequantise (one tile behind the copies, so that they overlap)
+  // fp8 cache: the stage and phase of the tile whose raw rows are the next to
+  // dequantise (one tile behind the copies, so that they overlap)
   int pend_stage = -1;
   uint32_t pend_ph = 0;
-  unsigned pend_valid = 0u;
   auto dequant_pending = [&]() -> bool {
     if (pend_stage < 0) return true;
     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.rawf[pend_stage]), pend_ph, abort,
                                            kErrTimeoutProducer)))
       return false;
-    attn_dequant_rows(&sm.kv[pend_stage][0][0], pend_valid, pw);
+    attn_dequant_rows(&sm.kv[pend_stage][0][0], pw);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sm.full[pend_stage]));
     pend_stage = -1;
@@ -434,30 +423,24 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
         // the raw row lands in the slot's last RAW_BYTES bytes; the warp dequantises
         // its rows of the previous tile while these copies are in flight
         const uint32_t rb = smem_u32(&sm.rawf[stage]);
-        if (lane == 0)
-          mbar_arrive_expect_tx(rb, __popc(valid & (0xFFu << (8 * pw))) * RAW_BYTES);
+        if (lane == 0) mbar_arrive_expect_tx(rb, AT_BK / AT_PRODUCERS * RAW_BYTES);
         __syncwarp();
-        if (mine && s >= 0)
+        if (mine)
           bulk_g2s(kv0 + (stage * AT_BK + lane) * AT_ROWB + (AT_ROWB - RAW_BYTES),
-                   kvb8 + s * a.ld_kv, RAW_BYTES, rb);
+                   s >= 0 ? kvb8 + s * a.ld_kv : zeros, RAW_BYTES, rb);
         if (!dequant_pending()) {
           ok = false;
           break;
         }
         pend_stage = stage;
         pend_ph = ph;
-        pend_valid = valid;
       } else {
         const uint32_t fb = smem_u32(&sm.full[stage]);
-        if constexpr (ADDR == kAddrPaged) {
-          attn_zero_rows(&sm.kv[stage][0][0], valid, pw);
-          __syncwarp();
-        }
-        if (lane == 0)
-          mbar_arrive_expect_tx(fb, __popc(valid & (0xFFu << (8 * pw))) * AT_ROW_BYTES);
+        if (lane == 0) mbar_arrive_expect_tx(fb, AT_BK / AT_PRODUCERS * AT_ROW_BYTES);
         __syncwarp();
-        if (mine && s >= 0)
-          bulk_g2s(kv0 + (stage * AT_BK + lane) * AT_ROWB, kvb + s * a.ld_kv, AT_ROW_BYTES, fb);
+        if (mine)
+          bulk_g2s(kv0 + (stage * AT_BK + lane) * AT_ROWB,
+                   s >= 0 ? static_cast<const void*>(kvb + s * a.ld_kv) : zeros, AT_ROW_BYTES, fb);
       }
       ++issued;
       if (++stage == AT_STAGES) {
@@ -726,12 +709,6 @@ __global__ void __launch_bounds__(AT_THREADS, 1)
     sm.abort = 0;
     fence_barrier_init();
   }
-  // rows a tile never receives (index < 0) keep whatever the buffer held; start from
-  // zeros so that those stale rows are always finite (their softmax weight is 0)
-  uint4* z = reinterpret_cast<uint4*>(&sm.kv[0][0][0]);
-  for (int i = threadIdx.x; i < static_cast<int>(sizeof(sm.kv) / 16); i += blockDim.x)
-    z[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
   __syncthreads();
   grid_dep_wait();  // set-up above touches no global memory
   if (threadIdx.x >= AT_CONSUMERS)

@@ -153,3 +153,72 @@ def test_fp32_with_separate_values():
         else:
             assert torch.equal(torch.isnan(l), torch.isnan(want)) and torch.isnan(o).all()
             assert (torch.isnan(want) | (l == want)).all()
+
+
+# -------------------------------------------- rows of one query do not reach another
+def _mixed_lists(R, n, k, g):
+    """Every third query selects rows 0..63 (which the tests fill with NaN and infinities),
+    the others fewer rows of the rest, so that their tiles keep places without a row."""
+    idx = torch.full((1, R, k), -1, dtype=torch.int32)
+    idx[0, 0::3, :64] = torch.arange(64, dtype=torch.int32)
+    for r in range(R):
+        if r % 3:
+            m = r % 40
+            idx[0, r, :m] = (64 + torch.randperm(n - 64, generator=g)[:m]).int()
+    return idx
+
+
+@pytest.mark.parametrize("R,ws", [(700, False), (300, True)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_contiguous_rows_stay_with_their_query(kind, R, ws):
+    g = torch.Generator().manual_seed(R)
+    n, k = 256, 64
+    x = torch.randn(n, 576, generator=g).bfloat16()
+    idx = _mixed_lists(R, n, k, g).to(DEV)
+    q = torch.randn(1, R, 16, 576, generator=g).bfloat16().to(DEV)
+    work = torch.empty(ic.ic_attn_workspace_size(1, R, 16, 512, k) + 16, dtype=torch.uint8,
+                       device=DEV) if ws else None
+    got = []
+    for bad in (False, True):
+        if bad:
+            x[0:64:2] = math.inf
+            x[1:64:2] = math.nan
+        cache = x.to(DEV) if kind == "bf16" else ic.ic_pack_kv_e4m3(x.to(DEV))
+        lse = torch.zeros(1, R, 16, device=DEV)
+        got.append((ic.ic_sparse_attn(q, cache[None], idx, 0.04, lse=lse, workspace=work), lse))
+        ic.ic_device_status()
+    others = [r for r in range(R) if r % 3]
+    for a, b in zip(*got):
+        assert torch.equal(a[0, others], b[0, others])
+    assert torch.isfinite(got[0][0]).all() and torch.isnan(got[1][0][0, 0::3]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_packed_sequences_rows_stay_with_their_sequence(fp8):
+    """Three sequences in shared launches; the first one's cache rows become NaN and inf."""
+    from tests.test_gpu_parity import _varlen_mla_case
+    lens = [400, 300, 333]
+    wl0, per, packed, desc = _varlen_mla_case(lens, "F,S", False, seed=3)
+    desc.attn_dtype = ic.IC_E4M3 if fp8 else ic.IC_BF16
+    desc.ld_kv = ic.KV8_ROW_BYTES if fp8 else 576
+    cu = [0, 400, 700, 1033]
+    ws = torch.empty(1033 * (wl0.L + 1) + 64, device=DEV)
+    got = []
+    for bad in (False, True):
+        t = torch.full((1033, wl0.k), -7, dtype=torch.int32, device=DEV)
+        layers = []
+        for e in packed:
+            kv = e["kv"].clone()
+            if bad:
+                kv[0:400:2] = math.inf
+                kv[1:400:2] = math.nan
+            layers.append(dict(e, kv=ic.ic_pack_kv_e4m3(kv) if fp8 else kv,
+                               out=torch.empty_like(e["out"]), lse=torch.empty_like(e["lse"])))
+        ic.ic_layer_stack_varlen("F,S", desc, layers, cu, t, ws)
+        ic.ic_device_status()
+        got.append((t, [e["out"] for e in layers], [e["lse"] for e in layers]))
+    assert torch.equal(got[0][0], got[1][0])
+    for l in range(2):
+        for a, b in zip(got[0][1:], got[1][1:]):
+            assert torch.equal(a[l][400:], b[l][400:]) and torch.isfinite(a[l][400:]).all()
+        assert torch.isnan(got[1][1][l][:400]).all()
