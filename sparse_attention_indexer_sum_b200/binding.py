@@ -695,9 +695,7 @@ def ic_cache_append(slots, *, kv=None, kv_cache=None, kv_dtype=None, k=None, k_c
             k_dt == IC_E4M3 else None, k_dt, count, flags)
 
 
-def make_paging(block_table, seq_lens, page_size: int, num_pages: int) -> ic_paging:
-    """ic_paging over block_table [batch, max_pages] int32 and seq_lens [batch] int32 (device
-    tensors that the caller keeps alive)."""
+def _paging(block_table, seq_lens, page_size, num_pages) -> ic_paging:
     if block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [batch, max_pages]")
     batch, cols = block_table.shape
@@ -711,6 +709,15 @@ def make_paging(block_table, seq_lens, page_size: int, num_pages: int) -> ic_pag
             not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be int32 [batch], contiguous")
     return ic_paging(block_table.data_ptr(), ld, cols, seq_lens.data_ptr(), page_size, num_pages)
+
+
+def make_paging(block_table, seq_lens, page_size: int, num_pages: int) -> ic_paging:
+    """ic_paging over block_table [batch, max_pages] int32 and seq_lens [batch] int32, device
+    tensors, which the result keeps alive."""
+    pg = _paging(block_table, seq_lens, page_size, num_pages)
+    _one_device(block_table, seq_lens)
+    pg.tensors = (block_table, seq_lens)
+    return pg
 
 
 def _pages(rows, page_size, name):
@@ -745,7 +752,7 @@ def ic_indexer_scores_paged(q, k_cache, w, block_table, seq_lens, *, page_size: 
             raise ValueError("e4m3 keys need fp32 q_scale [B, H] and k_scale [slots]")
         _contig(q_scale, k_scale)
     dev = _one_device(q, k_cache, w, block_table, seq_lens, scores, q_scale, k_scale)
-    pg = make_paging(block_table, seq_lens, page_size, _pages(slots, page_size, "k_cache"))
+    pg = _paging(block_table, seq_lens, page_size, _pages(slots, page_size, "k_cache"))
     most = cols * page_size
     if scores is None:
         scores = _new((B, most), torch.float32, dev, stream)
@@ -782,7 +789,7 @@ def ic_sparse_attn_paged(q, kv_cache, idx, block_table, seq_lens, scale: float, 
     _contig(q, idx, out, lse)
     kv_dtype, slots, ld = _kv_pool(kv_cache, kv_dtype)
     dev = _one_device(q, kv_cache, idx, block_table, seq_lens, out, lse, workspace)
-    pg = make_paging(block_table, seq_lens, page_size, _pages(slots, page_size, "kv_cache"))
+    pg = _paging(block_table, seq_lens, page_size, _pages(slots, page_size, "kv_cache"))
     if out is None:
         out = _new((B, R, H, 512), torch.bfloat16, dev, stream)
     elif out.dtype != torch.bfloat16 or out.shape != (B, R, H, 512):
@@ -799,12 +806,75 @@ def ic_sparse_attn_paged(q, kv_cache, idx, block_table, seq_lens, scale: float, 
     return out
 
 
+_CODES = {IC_BF16: (torch.bfloat16,), IC_E4M3: (torch.uint8, torch.float8_e4m3fn),
+          IC_MXF4: (torch.uint8,)}
+_F32 = (torch.float32,)
+
+
+def _holds(t, name, dtypes, count):
+    """Refuses a tensor that is not contiguous, of none of the types or of fewer elements."""
+    if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < count:
+        raise ValueError("%s must be contiguous %s of at least %d elements (got %s %s)" % (
+            name, " or ".join(str(d) for d in dtypes), count, t.dtype, tuple(t.shape)))
+
+
+def _check_step_paged(pattern, desc, paging, layers, t_cache, workspace) -> int:
+    """The device of a paged decode step's tensors.  Refuses tensors on several devices, and
+    those that hold less than desc and paging name, of another type, or with gaps.  Sizes and
+    formats that no tensor could fit, and missing tensors, are left to the library."""
+    B, rows = desc.batch, paging.num_pages * paging.page_size
+    used = list(getattr(paging, "tensors", ()))
+    if used and used[0].shape[0] < B:
+        raise ValueError("desc.batch is %d, the block table has %d rows" % (B, used[0].shape[0]))
+    if t_cache is not None:
+        _holds(t_cache, "t_cache", (torch.int32,), B * desc.k)
+        used.append(t_cache)
+    if workspace is not None:
+        _contig(workspace)
+        used.append(workspace)
+    heads = B * desc.heads
+    fields = {"q": ((torch.bfloat16,), heads * desc.dk), "out": ((torch.bfloat16,), heads * desc.dv),
+              "lse": (_F32, heads)}
+    codes = _CODES.get(desc.idx_dtype)
+    scores = {"q_idx": (codes, B * desc.H * desc.D), "k_idx": (codes, rows * desc.D),
+              "w": (_F32, B * desc.H)}
+    if desc.idx_dtype == IC_E4M3:
+        scores.update(q_scale=(_F32, B * desc.H), k_scale=(_F32, rows))
+    kv_codes = _CODES.get(desc.attn_dtype)
+    kinds = [c for c in pattern if c in "FS"]
+    for l, d in enumerate(layers):
+        want = {**fields, **scores} if kinds[l:l + 1] == ["F"] else fields
+        for f, (dtypes, count) in want.items():
+            t = d.get(f)
+            if t is not None:
+                if dtypes is not None:
+                    _holds(t, "layer %d: %s" % (l, f), dtypes, count)
+                used.append(t)
+        t = d.get("kv")
+        if t is not None:
+            if kv_codes is not None:
+                name, width = "layer %d: kv" % l, _KV_ROW[desc.attn_dtype] // t.element_size()
+                if t.is_contiguous():
+                    _holds(t, name, kv_codes, (rows - 1) * desc.ld_kv + width)
+                else:
+                    if t.dtype not in kv_codes or t.shape[-1] < width:
+                        raise ValueError("%s rows must be %s of at least %d elements" % (
+                            name, kv_codes[0], width))
+                    n, ld = _rows2d(t, name, t.shape[-1], t.dtype)
+                    if n < rows or ld != desc.ld_kv:
+                        raise ValueError("%s must hold %d rows, %d elements apart (got %d, %d)" % (
+                            name, rows, desc.ld_kv, n, ld))
+            used.append(t)
+    return _one_device(*used) if used else torch.cuda.current_device()
+
+
 def ic_decode_step_paged(pattern: str, desc: ic_stack_desc, paging: ic_paging, layers: list[dict],
                          t_cache, workspace, stream=None):
     """Decode step over paged caches (make_paging; desc.decode = 1, desc.L bounds the lengths):
-    layers hold the pools as k_idx, k_scale and kv."""
+    layers hold the pools as k_idx, k_scale and kv.  Runs on the tensors' device; tensors that
+    hold less than desc and paging name are refused."""
+    dev = _check_step_paged(pattern, desc, paging, layers, t_cache, workspace)
     arr = _layers(layers)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().ic_decode_step_paged(pattern.encode(), ctypes.byref(desc), ctypes.byref(paging),
-                                      arr, len(layers), _p(t_cache), _p(workspace), ws_bytes,
-                                      _stream(stream)))
+    _launch(dev, stream, lib().ic_decode_step_paged, pattern.encode(), ctypes.byref(desc),
+            ctypes.byref(paging), arr, len(layers), _ptr(t_cache), _ptr(workspace), ws_bytes)
