@@ -155,7 +155,8 @@ ic_status ic_indexer_scores(const void* q, const float* q_scale, const void* k,
  * lower index and -0 == +0 -- in ascending index order, padded with -1.
  *   scores [rows, ld] f32 (finite on the candidate columns), ld >= n
  *   idx    [rows, k] int32
- * 1 <= k <= 2048.  Bit-exact: the selection is a pure function of the fp32 values.
+ * 1 <= k <= 2048; n at most 2^31 - 4097.  Bit-exact: the selection is a pure function of the
+ * fp32 values.
  */
 ic_status ic_topk(const float* scores, long rows, int n, long ld, long pos0, int k, int* idx,
                   void* stream);
@@ -493,7 +494,8 @@ typedef struct {
  *   q [batch, H, D], q_scale [batch, H], w [batch, H], k [num_pages * page_size, D],
  *   k_scale [num_pages * page_size]: as ic_indexer_scores; dt = IC_BF16 or IC_E4M3
  *   (H = 64, D = 128; IC_F32 -> IC_ERR_UNSUPPORTED)
- *   scores [batch, ld] f32, ld >= max_len;  1 <= max_len <= max_pages * page_size
+ *   scores [batch, ld] f32, ld >= max_len;  1 <= max_len <= max_pages * page_size, and at
+ *   most 2^31 - 4097
  */
 ic_status ic_indexer_scores_paged(const void* q, const float* q_scale, const void* k,
                                   const float* k_scale, const float* w, ic_dtype dt, int batch,

@@ -216,6 +216,8 @@ static ic_status check_indexer_paged(const void* q, const float* q_scale, const 
                 max_len);
   if (static_cast<long>(batch) * 64 > 0x7fffffffL)
     return fail(IC_ERR_UNSUPPORTED, "indexer_paged: too many sequences");
+  if (max_len > kMaxScores)
+    return fail(IC_ERR_UNSUPPORTED, "indexer_paged: max_len above %d (got %d)", kMaxScores, max_len);
   return IC_OK;
 }
 

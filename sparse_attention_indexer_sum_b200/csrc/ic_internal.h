@@ -71,6 +71,10 @@ void trace_launch(int kind, cudaStream_t stream, double work);
 // Number of (query, key) pairs with key < Lk and key <= pos0 + r over rows r < R.
 long long causal_pairs(long R, long Lk, long pos0);
 
+// The longest row of scores: the kernels step through a row in 32-bit indices, up to 4096
+// past its end.
+constexpr int kMaxScores = 0x7fffffff - 4096;
+
 // Paged caches: token s of sequence b is pool row table[b, s >> shift] << shift plus
 // s's place in its page; a sequence holds min(seq_lens[b], max_len) tokens.
 struct PagedArgs {

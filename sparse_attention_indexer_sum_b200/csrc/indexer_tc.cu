@@ -845,6 +845,7 @@ __global__ void __launch_bounds__(IdxCfg<FP8, TPM, FUSED>::THREADS, 1)
           if (page >= 0 && page < a.pg.num_pages)
             ks = a.k_scale[(static_cast<long>(page) << a.pg.shift) +
                            (s & ((1 << a.pg.shift) - 1))];
+          static_assert(C::NSETS * C::BM <= 0x7fffffff - kMaxScores, "a step past the end");
           const int sn = s + C::NSETS * C::BM;
           pnext = sn < qi.Lk ? __ldg(row + (sn >> a.pg.shift)) : -1;
           pnext_qb = it.qb;

@@ -875,6 +875,9 @@ ic_status launch_topk_merge(const uint8_t* slots, long rows, long nt, long total
 
 ic_status launch_topk(const float* scores, long rows, int n, long ld, long pos0, int k, int* idx,
                       cudaStream_t stream, const int* valid_len) {
+  static_assert(4 * TK_THREADS <= 0x7fffffff - kMaxScores, "a step past the end of a row");
+  if (n > kMaxScores)
+    return fail(IC_ERR_UNSUPPORTED, "topk: rows of more than %d scores (got %d)", kMaxScores, n);
   if (rows == 0) return IC_OK;
   const int smem = static_cast<int>(sizeof(TopkSmem));
   ic_status st = cuda_check(
