@@ -99,13 +99,14 @@ struct E4m3Scale {
   }
 };
 
-__device__ __forceinline__ float block_sum(float v, float* part) {
+template <typename F>
+__device__ __forceinline__ F block_sum(F v, F* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int nw = blockDim.x / 32;
   if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
   __syncthreads();
-  float t = (threadIdx.x & 31) < nw ? part[threadIdx.x & 31] : 0.f;
+  F t = (threadIdx.x & 31) < nw ? part[threadIdx.x & 31] : F(0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
   return t;
@@ -181,18 +182,26 @@ __global__ void __launch_bounds__(1024, 2) rms_norm_kernel(const RmsNormArgs a) 
 // is read before the same thread writes it, so h may be the residual and y may be x.
 template <typename T>
 __global__ void __launch_bounds__(256) rms_norm_any_kernel(const RmsNormArgs a) {
-  __shared__ float part[32];
+  __shared__ double part[32];
   grid_dep_wait();
   const long row = blockIdx.x;
   const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
   const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.ld_r : nullptr;
-  float ss = 0.f;
-  for (int i = threadIdx.x; i < a.n; i += blockDim.x) {
-    float v = static_cast<float>(x[i]);
-    if (r) v += static_cast<float>(r[i]);
-    ss = fmaf(v, v, ss);
+  // a thread's squares in runs of 16, the runs in 64 bits: in one 32-bit sum the last of
+  // millions of terms would round to a fraction of their bits
+  double ss = 0.0;
+  for (int i = threadIdx.x; i < a.n;) {
+    const int end = min(a.n, i + 16 * static_cast<int>(blockDim.x));
+    float run = 0.f;
+#pragma unroll 4
+    for (; i < end; i += blockDim.x) {
+      float v = static_cast<float>(x[i]);
+      if (r) v += static_cast<float>(r[i]);
+      run = fmaf(v, v, run);
+    }
+    ss += run;
   }
-  const float total = block_sum(ss, part);
+  const float total = static_cast<float>(block_sum(ss, part));
   const float rstd = rsqrtf(total / static_cast<float>(a.n) + a.eps);
   T* h = a.h ? static_cast<T*>(a.h) + row * a.ld_h : nullptr;
   T* y = a.y ? static_cast<T*>(a.y) + row * a.ld_y : nullptr;
