@@ -414,9 +414,10 @@ size_t ic_stack_workspace_size(const ic_stack_desc* desc);
  *   scales   [rows, ceil(n / 128)] f32, dense (with codes): the groups' scales
  * At least one of y, codes and h is wanted.  Outputs may be inputs where the list says
  * so, with the same ld; otherwise they must not overlap.  1 <= n <= 2^30; every ld >= n (that
- * of an absent matrix is ignored); eps >= 0; |h| < 1.8e19 / sqrt(n), so that the sum of
- * squares stays finite.  Any alignment of the type is taken; rows of a multiple of 8
- * values, up to 16384, at 16-byte aligned addresses (codes: 8) are read only once.
+ * of an absent matrix is ignored); eps >= 0 (with 0, a row of zeros gives NaN);
+ * |h| < 1.8e19 / sqrt(n), so that the sum of squares stays finite.  Any alignment of the
+ * type is taken; rows of a multiple of 8 values, up to 16384, at 16-byte aligned addresses
+ * (codes: 8) are read only once.
  */
 ic_status ic_rms_norm(const void* x, long ld_x, const void* residual, long ld_r, ic_dtype dt,
                       const void* weight, ic_dtype w_dt, float eps, long rows, int n, void* h,

@@ -6,6 +6,8 @@
 //    e4m3 keys.
 // Both are bound by memory: every input is read once and every output written once,
 // from registers.
+#include <type_traits>
+
 #include "ic_device.cuh"
 #include "ic_internal.h"
 
@@ -112,6 +114,36 @@ __device__ __forceinline__ F block_sum(F v, F* part) {
   return t;
 }
 
+// The scale 1 / sqrt(mean(h^2) + eps) as up * rstd (y = h * up * rstd * weight).  WIDE: where
+// eps does not cover squares that vanish in 32 bits (kNormEps), they are taken and summed in
+// 64; up is a power of two that keeps both factors normal numbers where the scale is none.
+constexpr float kNormEps = 0x1p-100f;
+template <bool WIDE>
+struct NormSum {
+  using type = typename std::conditional<WIDE, double, float>::type;
+  static __device__ __forceinline__ void add(type& s, float v) {
+    if constexpr (WIDE)
+      s += static_cast<double>(v) * v;
+    else
+      s = fmaf(v, v, s);
+  }
+  float up = 1.f, rstd;
+  template <typename F>
+  __device__ __forceinline__ NormSum(F total, int n, float eps) {
+    if constexpr (WIDE) {
+      const double r = rsqrt(static_cast<double>(total) / n + eps);
+      up = r > 0x1p100 ? 0x1p64f : r < 0x1p-64 ? 0x1p-32f : 1.f;
+      rstd = static_cast<float>(r / up);
+    } else {
+      rstd = rsqrtf(static_cast<float>(total) / static_cast<float>(n) + eps);
+    }
+  }
+  __device__ __forceinline__ float operator()(float h, float w) const {
+    if constexpr (WIDE) h *= up;
+    return h * rstd * w;
+  }
+};
+
 // One CTA per row, the row in registers: thread t holds chunks t, t + T, ... of eight
 // values (CH of them at most; T = blockDim.x is a multiple of 32, so the 16 chunks of a
 // group of 128 lie in one half warp).
@@ -119,14 +151,15 @@ __device__ __forceinline__ F block_sum(F v, F* part) {
 // registers a thread instead of 40 (a few bytes spilled) take 16384 rows of 7168 with all
 // outputs from 190 to 173 us (6.1 TB/s, 0.93 of the measured copy rate), 4096 of 16384 from
 // 145 to 109 us.
-template <typename T, int CH>
+template <typename T, int CH, bool WIDE>
 __global__ void __launch_bounds__(1024, 2) rms_norm_kernel(const RmsNormArgs a) {
-  __shared__ float part[32];
+  using Sum = NormSum<WIDE>;
+  __shared__ typename Sum::type part[32];
   grid_dep_wait();
   const long row = blockIdx.x;
   const int chunks = a.n / 8;
   float v[CH][8];
-  float ss = 0.f;
+  typename Sum::type ss = 0;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
@@ -141,11 +174,10 @@ __global__ void __launch_bounds__(1024, 2) rms_norm_kernel(const RmsNormArgs a) 
         for (int j = 0; j < 8; ++j) v[i][j] += r[j];
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+      for (int j = 0; j < 8; ++j) Sum::add(ss, v[i][j]);
     }
   }
-  const float total = block_sum(ss, part);
-  const float rstd = rsqrtf(total / static_cast<float>(a.n) + a.eps);
+  const Sum scale(block_sum(ss, part), a.n, a.eps);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
@@ -157,7 +189,7 @@ __global__ void __launch_bounds__(1024, 2) rms_norm_kernel(const RmsNormArgs a) 
       else
         Vec8<__nv_bfloat16>::load(a.weight, 8 * c, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
+      for (int j = 0; j < 8; ++j) v[i][j] = scale(v[i][j], w[j]);
       if (a.y) Vec8<T>::store(a.y, row * a.ld_y + 8 * c, v[i]);
     }
     if (a.codes) {
@@ -180,7 +212,7 @@ __global__ void __launch_bounds__(1024, 2) rms_norm_kernel(const RmsNormArgs a) 
 // Any length, stride and alignment: one CTA per row, the row read twice (the second
 // time from cache), a warp per group of 128 values.  Every element of the second pass
 // is read before the same thread writes it, so h may be the residual and y may be x.
-template <typename T>
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) rms_norm_any_kernel(const RmsNormArgs a) {
   __shared__ double part[32];
   grid_dep_wait();
@@ -192,17 +224,16 @@ __global__ void __launch_bounds__(256) rms_norm_any_kernel(const RmsNormArgs a) 
   double ss = 0.0;
   for (int i = threadIdx.x; i < a.n;) {
     const int end = min(a.n, i + 16 * static_cast<int>(blockDim.x));
-    float run = 0.f;
+    typename NormSum<WIDE>::type run = 0;
 #pragma unroll 4
     for (; i < end; i += blockDim.x) {
       float v = static_cast<float>(x[i]);
       if (r) v += static_cast<float>(r[i]);
-      run = fmaf(v, v, run);
+      NormSum<WIDE>::add(run, v);
     }
     ss += run;
   }
-  const float total = static_cast<float>(block_sum(ss, part));
-  const float rstd = rsqrtf(total / static_cast<float>(a.n) + a.eps);
+  const NormSum<WIDE> scale(block_sum(ss, part), a.n, a.eps);
   T* h = a.h ? static_cast<T*>(a.h) + row * a.ld_h : nullptr;
   T* y = a.y ? static_cast<T*>(a.y) + row * a.ld_y : nullptr;
   const int lane = threadIdx.x & 31, groups = (a.n + 127) / 128;
@@ -218,7 +249,7 @@ __global__ void __launch_bounds__(256) rms_norm_any_kernel(const RmsNormArgs a) 
         if (h) h[i] = static_cast<T>(v[j]);
         const float w = a.w_f32 ? static_cast<const float*>(a.weight)[i]
                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(a.weight)[i]);
-        v[j] = v[j] * rstd * w;
+        v[j] = scale(v[j], w);
         if (y) y[i] = static_cast<T>(v[j]);
       }
       amax = fmaxf(amax, fabsf(v[j]));
@@ -237,7 +268,7 @@ __global__ void __launch_bounds__(256) rms_norm_any_kernel(const RmsNormArgs a) 
   }
 }
 
-template <typename T>
+template <typename T, bool WIDE>
 static cudaError_t launch_rms_norm_t(const RmsNormArgs& a, cudaStream_t stream) {
   const auto ok = [](const void* p, long ld_bytes, unsigned to) {
     return reinterpret_cast<uintptr_t>(p) % to == 0 && ld_bytes % to == 0;
@@ -247,7 +278,7 @@ static cudaError_t launch_rms_norm_t(const RmsNormArgs& a, cudaStream_t stream) 
                    ok(a.residual, a.ld_r * e, 16) && ok(a.h, a.ld_h * e, 16) &&
                    ok(a.y, a.ld_y * e, 16) && ok(a.codes, a.ld_c, 8) && ok(a.weight, 0, 16);
   const dim3 grid(static_cast<unsigned>(a.rows));
-  if (!vec) return launch_dep(rms_norm_any_kernel<T>, grid, dim3(256), 0, stream, 1, a);
+  if (!vec) return launch_dep(rms_norm_any_kernel<T, WIDE>, grid, dim3(256), 0, stream, 1, a);
   const int chunks = a.n / 8;
   // Two chunks a thread keep more CTAs, and so rows, in flight where there are rows to fill
   // them (16384 rows of 4096: 96 against 114 us); with few rows one chunk a thread is the
@@ -255,19 +286,23 @@ static cudaError_t launch_rms_norm_t(const RmsNormArgs& a, cudaStream_t stream) 
   const bool two = chunks > 1024 || (chunks > 128 && a.rows >= 4L * num_sms());
   const int per = two ? (chunks + 1) / 2 : chunks;
   const dim3 block(static_cast<unsigned>((per + 31) / 32 * 32));
-  return two ? launch_dep(rms_norm_kernel<T, 2>, grid, block, 0, stream, 1, a)
-             : launch_dep(rms_norm_kernel<T, 1>, grid, block, 0, stream, 1, a);
+  return two ? launch_dep(rms_norm_kernel<T, 2, WIDE>, grid, block, 0, stream, 1, a)
+             : launch_dep(rms_norm_kernel<T, 1, WIDE>, grid, block, 0, stream, 1, a);
 }
 
 ic_status launch_rms_norm(const RmsNormArgs& a, cudaStream_t stream) {
   if (a.rows == 0) return IC_OK;
-  ic_status st = cuda_check(a.f32 ? launch_rms_norm_t<float>(a, stream)
-                                  : launch_rms_norm_t<__nv_bfloat16>(a, stream),
-                            "rms_norm_kernel launch");
+  // (64 bits for every eps: 190 instead of 173 us on 16384 x 7168 with all outputs)
+  const cudaError_t e = a.eps < kNormEps
+                            ? a.f32 ? launch_rms_norm_t<float, true>(a, stream)
+                                    : launch_rms_norm_t<__nv_bfloat16, true>(a, stream)
+                        : a.f32 ? launch_rms_norm_t<float, false>(a, stream)
+                                : launch_rms_norm_t<__nv_bfloat16, false>(a, stream);
+  ic_status st = cuda_check(e, "rms_norm_kernel launch");
   if (!st) {
-    const double e = static_cast<double>(a.rows) * a.n, b = a.f32 ? 4.0 : 2.0;
+    const double m = static_cast<double>(a.rows) * a.n, b = a.f32 ? 4.0 : 2.0;
     trace_launch(kKindRmsNorm, stream,
-                 e * (b * (1 + (a.residual != nullptr) + (a.h != nullptr) + (a.y != nullptr)) +
+                 m * (b * (1 + (a.residual != nullptr) + (a.h != nullptr) + (a.y != nullptr)) +
                       (a.codes ? 1.0 : 0.0)) +
                      (a.codes ? 4.0 * a.rows * ((a.n + 127) / 128) : 0.0));
   }

@@ -44,3 +44,50 @@ def test_long_random_rows(dt, res):
     mag = (x.double().abs() + (0 if r is None else r.double().abs())) * gain
     lim = (17 / 2 + 5) * U_F32 * ref.abs() + 2 * U_F32 * mag + 1e-37
     assert ((y.double() - ref).abs() <= lim).all()
+
+
+@pytest.mark.parametrize("n", [8, 512, 509, 8200, 16384, 20001])
+@pytest.mark.parametrize("dt,size", [(torch.float32, 2.0 ** -140), (torch.float32, 2.0 ** -126),
+                                     (torch.float32, 2.0 ** -100), (torch.float32, 2.0 ** -72),
+                                     (torch.float32, 2.0 ** -40), (torch.float32, 2.0 ** 50),
+                                     (torch.bfloat16, 2.0 ** -120), (torch.bfloat16, 2.0 ** -70),
+                                     (torch.bfloat16, 2.0 ** 50)])
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-29])
+def test_rows_of_every_size(n, dt, size, eps):
+    """Small rows, whose squares vanish in 32 bits, with an eps that covers them and without;
+    the scale of such a row may itself be no normal 32-bit number.  (Squares of 2^50 and rows
+    of 20001 stay below the documented limit.)"""
+    g = torch.Generator().manual_seed(n)
+    x = ((torch.randn(3, n, generator=g).clamp(-6, 6) + 0.01).double() * size).to(dt).to(DEV)
+    x[2] = 1.0                             # a row of ordinary size beside them
+    w = (1 + 0.2 * torch.randn(n, generator=g)).to(DEV)
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    codes = torch.empty(3, n, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(3, -(-n // 128), device=DEV)
+    ic.ic_rms_norm(x, w, eps, h=h, y=y, codes=codes, scales=scales)
+    ic.ic_device_status()
+    assert torch.equal(h, x)
+    xd = x.double()
+    eps32 = float(torch.tensor(eps, dtype=torch.float32))   # as the call takes it
+    ref = xd / (xd.pow(2).mean(-1, keepdim=True) + eps32).sqrt() * w.double()
+    assert ref[:2].abs().amax() > 0.1 or eps > size ** 2 / 100
+    # the sum (n / 256 + 11 terms at most in a chain, halved by the root), the root and the
+    # products; a result below the normal numbers keeps half a step of the smallest
+    rel = ((min(n, 16384) / 256 + 17) / 2 + 8) * U_F32
+    u = torch.finfo(dt).eps / 2
+    tiny = 2.0 ** -149 if dt == torch.float32 else 2.0 ** -133
+    assert ((y.double() - ref).abs() <= (u + rel * (1 + u)) * ref.abs() + tiny).all()
+    m = -(-n // 128)
+    pad = torch.nn.functional.pad(ref, (0, m * 128 - n)).unflatten(-1, (m, 128))
+    want = pad.abs().amax(-1) / 448
+    assert ((scales.double() - want).abs() <= (rel + 4 * U_F32) * want + 2.0 ** -148).all()
+
+
+@pytest.mark.parametrize("n", [512, 509])
+def test_zero_rows(n):
+    x = torch.zeros(2, n, device=DEV)
+    w = torch.ones(n, device=DEV)
+    assert (ic.ic_rms_norm(x, w, 1e-6)[0] == 0).all()
+    assert (ic.ic_rms_norm(x, w, 2.0 ** -149)[0] == 0).all()
+    assert torch.isnan(ic.ic_rms_norm(x, w, 0.0)[0]).all()     # 0 / 0
+    ic.ic_device_status()
