@@ -37,10 +37,12 @@
  *    ic_device_status() reports it (IC_ERR_TIMEOUT).
  *  - libic_b200_debug.so, the same library built with -DIC_DEBUG_BOUNDS, also
  *    checks the indices its kernels compute (index-list entries against their
- *    cache, TMA tile coordinates, top-k and merge output slots) before using
- *    them; a failed check skips the access and ic_device_status() reports
- *    IC_ERR_BOUNDS.  (Index-list entries outside the cache are skipped in every
- *    build; only the debug build reports them.)
+ *    cache, page numbers against their pool, TMA tile coordinates, top-k and
+ *    merge output slots) before using them; a failed check skips the access and
+ *    ic_device_status() reports IC_ERR_BOUNDS.  (Index-list entries outside the
+ *    cache are skipped in every build; only the debug build reports them.  The
+ *    paged calls allow entries past a sequence's length, and the cache append
+ *    tokens without a slot: neither is reported.)
  */
 #ifndef IC_H_
 #define IC_H_

@@ -568,7 +568,6 @@ ic_status ic_device_status(void* stream) {
                   : v == kErrBoundsTma  ? "TMA tile coordinate outside the tensor"
                   : v == kErrBoundsTopk ? "top-k output slot outside the row"
                   : v == kErrBoundsPage ? "page number outside the pool"
-                  : v == kErrBoundsSlot ? "cache slot or position outside its cache or table"
                                         : "merge slot or piece count out of range");
     return fail(IC_ERR_TIMEOUT, "device error word %d (a bounded device wait gave up)", v);
   }

@@ -391,7 +391,7 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
     auto pool_row = [&](int t) -> long {
       const int j = t * AT_BK + lane;
       const int s = (t < ntiles && j < cnt) ? ilist[j] : -1;
-      if (!in_bounds(s >= -1 && s < lkv, kErrBoundsGather) || s < 0 || s >= lkv) return -1;
+      if (s < 0 || s >= lkv) return -1;  // (entries past the sequence are allowed here)
       if constexpr (ADDR == kAddrPaged) return attn_page_row(sg, kr0, s);
       return s;
     };

@@ -277,7 +277,7 @@ __device__ __forceinline__ void packed_producer(PackedSmem<FMT>& sm, const AttnA
     auto pool_row = [&](int t) -> int {
       const int j = t * PK_BK + lane;
       const int s = (t < ntiles && j < cnt) ? ilist[j] : -1;
-      if (!in_bounds(s >= -1 && s < len, kErrBoundsGather) || s < 0 || s >= len) return -1;
+      if (s < 0 || s >= len) return -1;
       return static_cast<int>(attn_page_row(pg, b, s));
     };
     // the groups take turns: whole rounds of them, at least one

@@ -356,10 +356,7 @@ __global__ void __launch_bounds__(128, 10) cache_append_kernel(const AppendArgs 
   }
   if (a.k) ku = *reinterpret_cast<const uint2*>(a.k + row * a.ld_k + 4 * lane);
   if (slot < 0) return;  // a padded row
-  if (!in_bounds(slot < a.num_slots && pos >= 0 && (!a.rope || pos < a.rope_rows),
-                 kErrBoundsSlot) ||
-      slot >= a.num_slots || pos < 0 || (a.rope && pos >= a.rope_rows))
-    return;
+  if (slot >= a.num_slots || pos < 0 || (a.rope && pos >= a.rope_rows)) return;
   const bool turn = a.rope != nullptr;
   float rc = 0.f, rs = 0.f;  // cos and sin of angle l
   if (turn) {

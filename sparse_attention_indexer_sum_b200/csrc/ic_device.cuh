@@ -39,7 +39,6 @@ enum DevErr : int {
   kErrBoundsTopk = 18,    // a top-k output slot or index outside its row
   kErrBoundsMerge = 19,   // a merge output slot or piece count out of range
   kErrBoundsPage = 20,    // a page number outside the pool
-  kErrBoundsSlot = 21,    // a cache slot or position outside its cache or table
 };
 
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_dev_error, 0, code); }
