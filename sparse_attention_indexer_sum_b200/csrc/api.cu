@@ -166,6 +166,9 @@ static ic_status check_desc(const ic_stack_desc* d, bool decode) {
     return fail(IC_ERR_INVALID_ARG, decode ? "decode step needs desc->decode = 1"
                                            : "layer stack needs desc->decode = 0 (use ic_decode_step)");
   if (!decode && d->batch != 1) return fail(IC_ERR_UNSUPPORTED, "stack: prefill batch must be 1");
+  if (d->L > kMaxScores)
+    return fail(IC_ERR_UNSUPPORTED, "stack: L above the max_len of a row of scores, %d (got %d)", kMaxScores,
+                d->L);
   return IC_OK;
 }
 

@@ -41,3 +41,13 @@ def test_paged_indexer_and_step(lib, n):
 
 def test_no_rows_of_the_longest_length_are_fine(lib):
     assert lib.ic_topk(FAKE, 0, MOST, MOST, -1, 64, FAKE, None) == binding.IC_OK
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_contiguous_stacks_launch_nothing_for_rows_that_the_topk_refuses(lib, decode):
+    io = binding.ic_layer_io(q_idx=256, k_idx=256, w=256, q=256, kv=256, v=256, out=256)
+    d = binding.make_desc(L=MOST + 1, k=64, H=1, D=1, idx_dtype=binding.IC_F32, heads=1, dk=1,
+                          dv=1, attn_dtype=binding.IC_F32, scale=1.0, batch=1, decode=decode)
+    f = lib.ic_decode_step if decode else lib.ic_layer_stack
+    st = f(b"F", ctypes.byref(d), (binding.ic_layer_io * 1)(io), 1, FAKE, FAKE, 1 << 40, None)
+    assert st == binding.IC_ERR_UNSUPPORTED and "L above the max_len" in binding.ic_last_error()
