@@ -386,20 +386,22 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
     }
     const int nt = ntiles > 0 ? ntiles : 1;  // an empty item still ends with one (empty) tile
     bool ok = true;
-    // paged: the pool row of this lane's entry of tile t (the page table is read one
-    // tile ahead, so that its latency hides behind the wait for a free stage)
-    auto pool_row = [&](int t) -> long {
+    // the cache row of this lane's entry of tile t, or -1.  Paged: the page table is read
+    // one tile ahead, so that its latency hides behind the wait for a free stage; entries
+    // past the sequence are allowed.
+    auto cache_row = [&](int t) -> long {
       const int j = t * AT_BK + lane;
       const int s = (t < ntiles && j < cnt) ? ilist[j] : -1;
-      if (s < 0 || s >= lkv) return -1;  // (entries past the sequence are allowed here)
-      if constexpr (ADDR == kAddrPaged) return attn_page_row(sg, kr0, s);
-      return s;
+      if constexpr (ADDR == kAddrPaged)
+        return s < 0 || s >= lkv ? -1 : attn_page_row(sg, kr0, s);
+      else
+        return !in_bounds(s >= -1 && s < lkv, kErrBoundsGather) || s >= lkv ? -1 : s;
     };
     long prow = -1;
-    if constexpr (ADDR == kAddrPaged) prow = pool_row(0);
+    if constexpr (ADDR == kAddrPaged) prow = cache_row(0);
     for (int t = 0; t < nt; ++t) {
       long pnext = -1;
-      if constexpr (ADDR == kAddrPaged) pnext = pool_row(t + 1);
+      if constexpr (ADDR == kAddrPaged) pnext = cache_row(t + 1);
       if (!mbar_wait(smem_u32(&sm.empty[stage]), ph ^ 1, abort, kErrTimeoutProducer)) {
         ok = false;
         break;
@@ -409,10 +411,7 @@ __device__ __forceinline__ void attn_producer(AttnSmem& sm, const AttnArgs& a,
         s = prow;
         prow = pnext;
       } else {
-        const int j = t * AT_BK + lane;
-        int e = (t < ntiles && j < cnt) ? ilist[j] : -1;
-        if (!in_bounds(e >= -1 && e < lkv, kErrBoundsGather) || e >= lkv) e = -1;
-        s = e;
+        s = cache_row(t);
       }
       const unsigned valid = __ballot_sync(0xffffffffu, s >= 0);
       if (pw == 0 && lane == 0) {

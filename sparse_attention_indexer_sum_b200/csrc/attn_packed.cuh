@@ -59,6 +59,7 @@ constexpr int PK_THREADS = PK_CONSUMERS + 32 * PK_PROD_WARPS;
 constexpr int PK_CREGS = 216, PK_PREGS = 72;
 static_assert(PK_CONSUMERS * PK_CREGS + 32 * PK_PROD_WARPS * PK_PREGS <= 168 * PK_THREADS,
               "the split must not exceed what the block was launched with");
+static_assert(PK_GROUPS == 2, "group 0 merges group 1's part of an item");
 static_assert(PK_PROD_WARPS == 4 && PK_BK == 32, "whole warpgroups change registers; a lane per row");
 constexpr int PK_SROW = PK_BK + 8;              // padded partial-score row (floats)
 constexpr int PK_PROW = PK_BK + 8;              // padded P row (bf16)
@@ -105,7 +106,7 @@ struct PackedSmem {
   alignas(128) PackedStage<FMT> raw[STAGES];
   PackedGroup grp[PK_GROUPS];
   alignas(128) uint8_t q[AT_H][AT_ROWB];
-  alignas(16) float4 o1[PK_GROUPS - 1][AT_H * AT_DV / 4];  // the other groups' O at an item's end
+  alignas(16) float4 o1[AT_H * AT_DV / 4];  // group 1's O at an item's end
   alignas(16) int ibuf[2][AT_MAXK];
   uint32_t vmask[STAGES];  // bit j: row j has an entry
   int last[STAGES];
@@ -115,7 +116,7 @@ struct PackedSmem {
   uint64_t qfull, qempty;
   uint64_t ifull[2];
   uint64_t pitem;
-  uint64_t xfull, xempty;  // an item's O and sums of the groups but the first
+  uint64_t xfull, xempty;  // group 1's O and sums of an item
   int abort;
 };
 static_assert(sizeof(PackedSmem<kFmtMxf4>) <= 232448 && sizeof(PackedSmem<kFmtE4m3>) <= 232448,
@@ -658,7 +659,7 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
     // this lane holds dims 128 warp + 32 cq..+32 of heads g (o[.][0..1]) and g + 8
     // (o[.][2..3]), placed as PackedFmt::reg says; group 1 leaves four floats per (j, lane)
     if (grp > 0) {
-      float4* dst = sm.o1[grp - 1] + warp * 512 + lane;
+      float4* dst = sm.o1 + warp * 512 + lane;
 #pragma unroll
       for (int j = 0; j < 16; ++j) dst[32 * j] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
       __syncwarp();
@@ -667,24 +668,22 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
       named_bar_sync(1 + grp, PK_GTHREADS);  // fin_m, fin_l of this group
       ok = __all_sync(0xffffffffu, wait(sm.xfull, it & 1));
       if (!ok) continue;
-      float wt[PK_GROUPS][2], M[2], L[2];  // heads g, g + 8: the groups' weights
+      float wt[2][2], M[2], L[2];  // the groups' weights, and their sums: heads g, g + 8
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int h = g + 8 * hh;
-        M[hh] = sm.grp[0].fin_m[h];
-#pragma unroll
-        for (int x2 = 1; x2 < PK_GROUPS; ++x2) M[hh] = fmaxf(M[hh], sm.grp[x2].fin_m[h]);
+        M[hh] = fmaxf(sm.grp[0].fin_m[h], sm.grp[1].fin_m[h]);
         L[hh] = 0.f;
 #pragma unroll
-        for (int x2 = 0; x2 < PK_GROUPS; ++x2) {
+        for (int x2 = 0; x2 < 2; ++x2) {
           const float m = sm.grp[x2].fin_m[h];
           wt[x2][hh] = m == -INFINITY ? 0.f : fast_exp2(m - M[hh]);
           L[hh] += sm.grp[x2].fin_l[h] * wt[x2][hh];
         }
         if (!a.split) {
           const float inv = L[hh] > 0.f ? 1.f / L[hh] : 0.f;
-#pragma unroll
-          for (int x2 = 0; x2 < PK_GROUPS; ++x2) wt[x2][hh] *= inv;
+          wt[0][hh] *= inv;
+          wt[1][hh] *= inv;
         }
       }
 #pragma unroll
@@ -693,14 +692,11 @@ __device__ __forceinline__ void packed_consumer(PackedSmem<FMT>& sm, const AttnA
         o[j][1] *= wt[0][0];
         o[j][2] *= wt[0][1];
         o[j][3] *= wt[0][1];
-#pragma unroll
-        for (int x2 = 1; x2 < PK_GROUPS; ++x2) {
-          const float4 u = sm.o1[x2 - 1][warp * 512 + lane + 32 * j];
-          o[j][0] += u.x * wt[x2][0];
-          o[j][1] += u.y * wt[x2][0];
-          o[j][2] += u.z * wt[x2][1];
-          o[j][3] += u.w * wt[x2][1];
-        }
+        const float4 u = sm.o1[warp * 512 + lane + 32 * j];
+        o[j][0] += u.x * wt[1][0];
+        o[j][1] += u.y * wt[1][0];
+        o[j][2] += u.z * wt[1][1];
+        o[j][3] += u.w * wt[1][1];
       }
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -769,7 +765,7 @@ __global__ void __launch_bounds__(PK_THREADS, 1)
     mbar_init(smem_u32(&sm.ifull[0]), 1);
     mbar_init(smem_u32(&sm.ifull[1]), 1);
     mbar_init(smem_u32(&sm.pitem), PK_PROD_WARPS);
-    mbar_init(smem_u32(&sm.xfull), (PK_GROUPS - 1) * PK_GTHREADS / 32);
+    mbar_init(smem_u32(&sm.xfull), PK_GTHREADS / 32);
     mbar_init(smem_u32(&sm.xempty), PK_GTHREADS / 32);
     sm.abort = 0;
     fence_barrier_init();
