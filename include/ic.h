@@ -457,7 +457,7 @@ ic_status ic_rms_norm(const void* x, long ld_x, const void* residual, long ld_r,
  *         k_scale [num_slots], quantised as by ic_quant_e4m3_rows but from the rotated
  *         fp32 values
  * kv, kv_cache and k_cache are 16-byte aligned, k is 8-byte aligned; ld_kv is a multiple
- * of 8 and ld_k of 4.
+ * of 8 and ld_k of 4.  Inputs do not overlap the caches.
  */
 #define IC_ROPE_KV_HALVES 1
 #define IC_ROPE_K_HALVES 2

@@ -22,12 +22,15 @@
 // number value * 2^-126 (0.5 becomes a subnormal); one AND, one multiplication (both
 // shifts at once) and one AND move two codes, and a bf16 multiplication by 2^(E - 1)
 // gives two exact scaled values.  e4m3 expansion: to fp32, times the scale, rounded to bf16
-// (the one rounding of V and K here; the bf16 operands are what the MMA multiplies).
+// (the bf16 operands are what the MMA multiplies; 4-bit rows need no such rounding).
+// Probabilities are rounded to bf16 for the product with V, as in attn_mla_kernel (off by 2^-8
+// of their size at most, as the bf16 output is).  Their sum is that of the unrounded ones, in
+// 32 bits, as are scores and O.
 //
 // Measured, 4-bit rows: 3 x 341 queries of 2048 rows of 40000 (2.1 M rows, 7.3e10 flop; L2
 // holds the cache) in 375 us = 195 TFLOP/s, 0.12 of the measured bf16 rate; bf16 rows take
-// 394 us there in attn_mla_kernel, e4m3 rows 472 us.  64 decode queries over 64 x 200000
-// rows, with the merge: 39 us (52 MB of rows, 8 us at the measured HBM rate); bf16 46 us,
+// 392 us there in attn_mla_kernel, e4m3 rows 472 us.  64 decode queries over 64 x 200000
+// rows, with the merge: 38 us (52 MB of rows, 8 us at the measured HBM rate); bf16 44 us,
 // e4m3 47 us.  A tile of 32 keys costs an SM 1550 cycles; its products alone are 68 x 9
 // cycles of each tensor pipe (the warp-level MMA at M = 16 heads) and its expansion 600 of
 // each integer pipe, but one group's chain is twice that: by the clock, loads, expansion and
@@ -76,7 +79,8 @@ struct PackedFmt {
                 "every use of a stage falls to one group and one producer");
   // pairs of rows that a producer's loop copies in a piece: all 16 of a 4-bit tile (with 4:
   // 385 instead of 375 us on 3 x 341 queries), 4 of an e4m3 tile, whose rows take more
-  // instructions and spill the producers' registers otherwise (16: 479 instead of 472 us)
+  // instructions and spill more registers otherwise (68 instead of 40 bytes; 16: 479 instead
+  // of 472 us)
   static constexpr int COPY_PAIRS = MX ? 16 : 4;
   // The register that holds dim d (0..7) of the eight dims i of a lane's 32, among v[n] or
   // o, and its half: the pairs are (0, 4), (1, 5), .. as the 4-bit expansion makes them, or
